@@ -14,6 +14,12 @@ Torch conveniences:
     chunk_forward_scalar(q, k, v, alpha, beta, S0=None, chunk=64) -> (o, S_T)
     chunk_forward_varlen(q, k, v, a, b, w, cu_seqlens, S0=None, chunk=64) -> (o, S_T)
     decode_step(q, k, v, a, b, w, S) -> o        (S updated in place)
+Next to the delta rule (raw gdn2_linear_*, gdn2_norm_*, gdn2_state_cache_* as well):
+    linear_forward(x, a, b, h0=None, gates="channel") -> (o, h_T)   h_t = a_t h_{t-1} + b_t x_t
+    linear_forward_varlen, linear_step, linear_backward, linear_backward_varlen,
+    gated_linear_recurrence, gated_linear_recurrence_varlen (autograd)
+    norm_forward(x, weight, bias, gate, eps, kind) -> y, norm_backward, norm (autograd)
+    state_cache_empty, state_cache_store, state_cache_load          (states in 8 bits)
 
 If ``libgdn2.so`` has not been built, loading fails loudly: there is no
 fallback path.
@@ -49,6 +55,11 @@ EXPORTED = ("gdn2_chunk_forward", "gdn2_chunk_forward_coupled", "gdn2_chunk_forw
             "gdn2_chunk_backward_varlen", "gdn2_chunk_backward_varlen_workspace_bytes", "gdn2_chunk_backward_preact",
             "gdn2_chunk_backward_coupled", "gdn2_chunk_backward_scalar", "gdn2_chunk_forward_varlen_gates",
             "gdn2_chunk_backward_varlen_gates", "gdn2_decode_step_gates",
+            "gdn2_linear_forward", "gdn2_linear_forward_workspace_bytes", "gdn2_linear_forward_varlen",
+            "gdn2_linear_forward_varlen_workspace_bytes", "gdn2_linear_step", "gdn2_linear_backward",
+            "gdn2_linear_backward_workspace_bytes", "gdn2_linear_backward_varlen",
+            "gdn2_linear_backward_varlen_workspace_bytes", "gdn2_norm_forward", "gdn2_norm_backward",
+            "gdn2_norm_backward_workspace_bytes", "gdn2_state_cache_store", "gdn2_state_cache_load",
             "gdn2_status_string", "gdn2_version")
 
 
@@ -115,6 +126,8 @@ def load(path: Optional[str] = None):
     lib.gdn2_chunk_backward_varlen.argtypes = [dp] + [vp] * 17 + [vp, sz, vp]
     lib.gdn2_chunk_backward_varlen_workspace_bytes.restype = sz
     lib.gdn2_chunk_backward_varlen_workspace_bytes.argtypes = [dp]
+    for part in (linear, norms, state_cache):
+        part.declare(lib)
     lib.gdn2_status_string.restype = ctypes.c_char_p
     lib.gdn2_status_string.argtypes = [ctypes.c_int]
     lib.gdn2_version.restype = ctypes.c_int
@@ -801,3 +814,18 @@ def gated_delta_rule_varlen(q, k, v, a, b, w, cu_seqlens, S0=None, chunk: int = 
     if _GDR2V is None:
         _GDR2V = _autograd_function_varlen()
     return _GDR2V.apply(q, k, v, a, b, w, cu_seqlens, S0, chunk, gates)
+
+
+# ------------------------------------------------------------------ next to the delta rule
+from . import linear, norms, state_cache  # noqa: E402  (they take the helpers above)
+from .linear import (LINEAR_CHECKPOINT, LINEAR_GATES, gated_linear_recurrence,  # noqa: E402,F401
+                     gated_linear_recurrence_varlen, gdn2_linear_backward, gdn2_linear_backward_varlen,
+                     gdn2_linear_backward_varlen_workspace_bytes, gdn2_linear_backward_workspace_bytes,
+                     gdn2_linear_desc, gdn2_linear_forward, gdn2_linear_forward_varlen,
+                     gdn2_linear_forward_varlen_workspace_bytes, gdn2_linear_forward_workspace_bytes,
+                     gdn2_linear_step, linear_backward, linear_backward_varlen, linear_forward,
+                     linear_forward_varlen, linear_step)
+from .norms import (NORM_KINDS, gdn2_norm_backward, gdn2_norm_backward_workspace_bytes, gdn2_norm_desc,  # noqa: E402,F401
+                    gdn2_norm_forward, norm, norm_backward, norm_forward)
+from .state_cache import (CACHE_FORMATS, gdn2_cache_desc, gdn2_state_cache_load, gdn2_state_cache_store,  # noqa: E402,F401
+                          state_cache_empty, state_cache_load, state_cache_store)

@@ -5,32 +5,20 @@
 
 #include <stdint.h>
 
+#include "gdn2_check.hpp"
 #include "gdn2_internal.hpp"
 #include "gdn2_range.hpp"
 
 namespace {
 
+using gdn2::aligned16;
+using gdn2::aligned4;
+using gdn2::overlaps;
+using gdn2::Range;
+using gdn2::range_of;
+
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void *p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, lo + bytes};
-}
-
-bool overlaps(Range x, Range y) {
-  return x.lo != x.hi && y.lo != y.hi && x.lo < y.hi && y.lo < x.hi;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// One fp32 per token and value head (beta, alpha and their gradients) is read
-// and written as single floats: 4-byte alignment, so that a view starting at
-// any token of a [T, H_v] tensor is accepted.
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Common description checks; `decode` additionally requires T == 1.
 gdn2_status check_desc(const gdn2_desc *d, bool decode) {

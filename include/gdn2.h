@@ -432,6 +432,186 @@ gdn2_status gdn2_chunk_backward_varlen_gates(const gdn2_desc *desc, const int32_
                                              void *dw, float *dS0, void *workspace, size_t workspace_bytes,
                                              void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence: the delta rule's diagonal sibling, one fp32 state
+ * per channel,
+ *
+ *   h_t = a_t * h_{t-1} + b_t * x_t,      o_t = h_t      (channel by channel)
+ *
+ * for layers that mix a sequence without keys and queries. The conventions
+ * above hold (device pointers, contiguous row-major tensors, argument errors
+ * before anything is enqueued, no state between calls), but tensors need only
+ * be aligned to their elements: a view that starts at any token is accepted.
+ *   x, o      : [B, T, D] in the input dtype
+ *   a, b      : [B, T, D], by gate form (below)
+ *   h0, h_T   : [B, D] fp32
+ * Any B, T >= 0 and D >= 1; T <= 2^31 - 257 and B * ceil(T / 128) *
+ * ceil(D / 64) <= 2^24 - 1 (GDN2_ERR_UNSUPPORTED beyond). Where D is a
+ * multiple of 4 and every tensor 16-byte aligned, rows are moved with wide loads.
+ *
+ * Gate forms:
+ *   GDN2_LINEAR_CHANNEL     : a decay, b input gate, fp32
+ *   GDN2_LINEAR_PREACT      : pre-activations in the input dtype, activated in
+ *                             the kernel: a = exp(-softplus(a_pre)),
+ *                             b = sigmoid(b_pre) (as gdn2_chunk_forward_preact;
+ *                             magnitudes above 87 count as 87)
+ *   GDN2_LINEAR_TIED        : b = 1 - a, a fp32; the argument b is unused
+ *   GDN2_LINEAR_TIED_PREACT : b = 1 - a, a from its pre-activation; b unused
+ * Preconditions, not checked: a in [0, 1], finite inputs (NaN and infinities
+ * propagate within their sequence and channel). States and sums are fp32; o
+ * and bf16 gradients are rounded once. Results are deterministic. */
+typedef enum {
+  GDN2_LINEAR_CHANNEL = 0,
+  GDN2_LINEAR_PREACT = 1,
+  GDN2_LINEAR_TIED = 2,
+  GDN2_LINEAR_TIED_PREACT = 3
+} gdn2_linear_gates;
+
+/* gates: a gdn2_linear_gates; dtype: a gdn2_dtype for x, o (and the gates and
+ * their gradients in the pre-activation forms). */
+typedef struct {
+  int32_t B, T, D;
+  int32_t gates, dtype;
+} gdn2_linear_desc;
+
+/* Tokens between two saved states (ck below). */
+#define GDN2_LINEAR_CHECKPOINT 128
+
+/* Whole sequences.
+ *   h0  : may be NULL (zero).   h_T : may be NULL, may be h0 itself.
+ *   ck  : may be NULL; otherwise [B, ceil(T / 128), D] fp32:
+ *         the states entering tokens 128, 256, ... of every sequence, which
+ *         the backward takes (row 0 of each sequence is not written).
+ *   o   : may be NULL if ck or h_T is wanted alone.
+ *   workspace: gdn2_linear_forward_workspace_bytes(desc) bytes, 16-byte
+ *         aligned (NULL if that is 0); scratch on entry and exit.
+ * An output that overlaps an input, the workspace or another output is
+ * GDN2_ERR_ALIAS (but h_T == h0). T == 0: h_T = h0 (or zeros). */
+size_t gdn2_linear_forward_workspace_bytes(const gdn2_linear_desc *desc);
+gdn2_status gdn2_linear_forward(const gdn2_linear_desc *desc, const void *x, const void *a, const void *b,
+                                const float *h0, void *o, float *h_T, float *ck, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* B sequences packed along T tokens: x, a, b, o are [T, D], sequence n is
+ * tokens cu_seqlens[n] .. cu_seqlens[n+1]-1 (B + 1 non-decreasing int32 device
+ * offsets, clamped to [0, T]; they need not cover all T tokens: rows of o
+ * outside every sequence are left as they were). h0, h_T: [B, D]; an empty
+ * sequence gives h_T = h0. ck: [ceil(T / 128), D], the state entering every
+ * 128th token of the packed axis where that token continues a sequence
+ * (other rows are not written). */
+size_t gdn2_linear_forward_varlen_workspace_bytes(const gdn2_linear_desc *desc);
+gdn2_status gdn2_linear_forward_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens, const void *x,
+                                       const void *a, const void *b, const float *h0, void *o, float *h_T, float *ck,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token per sequence (desc->T must be 1): h_out = a * h + b * x, o = h_out
+ * in the input dtype. h, h_out: [B, D] fp32; h_out may be h (in place), but
+ * not a partial overlap. */
+gdn2_status gdn2_linear_step(const gdn2_linear_desc *desc, const void *x, const void *a, const void *b,
+                             const float *h, float *h_out, void *o, void *stream);
+
+/* Gradients of gdn2_linear_forward, given dO = dLoss/do (input dtype) and
+ * dh_T = dLoss/dh_T (fp32, or NULL: zero).
+ *   dx : [B, T, D] input dtype.   da, db : the shapes and types of a and b
+ *        (pre-activation forms: with respect to the pre-activations; tied
+ *        forms: da through both uses of a, db unused).
+ *   dh0: [B, D] fp32, or NULL; may be dh_T itself.
+ *   ck : the states the forward saved, or NULL: they are computed again into
+ *        the workspace, which costs one more pass over x, a and b.
+ * The states are walked again from ck in fp32: no rounded output is read.
+ * workspace: gdn2_linear_backward_workspace_bytes(desc) bytes, 16-byte
+ * aligned. Errors as for the forward. */
+size_t gdn2_linear_backward_workspace_bytes(const gdn2_linear_desc *desc);
+gdn2_status gdn2_linear_backward(const gdn2_linear_desc *desc, const void *x, const void *a, const void *b,
+                                 const float *h0, const float *ck, const void *dO, const float *dh_T, void *dx,
+                                 void *da, void *db, float *dh0, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Gradients of gdn2_linear_forward_varlen. Gradient rows outside every
+ * sequence are left as they were; an empty sequence gives dh0 = dh_T. */
+size_t gdn2_linear_backward_varlen_workspace_bytes(const gdn2_linear_desc *desc);
+gdn2_status gdn2_linear_backward_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens, const void *x,
+                                        const void *a, const void *b, const float *h0, const float *ck,
+                                        const void *dO, const float *dh_T, void *dx, void *da, void *db, float *dh0,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Norms over the last axis, for the keys and queries of a mixing layer, its
+ * heads' outputs (with their output gate) and the model width:
+ *
+ *   c = x - mean(x) (GDN2_NORM_LAYER) or x (GDN2_NORM_RMS)
+ *   y = (c / sqrt(mean(c^2) + eps) * weight + bias) * silu(gate)
+ *
+ *   x, gate, y : [rows, D] in desc->dtype; gate may be NULL (no factor)
+ *   weight, bias : [D] in desc->wdtype; either may be NULL (ones, zeros)
+ * Any rows >= 0, D >= 1; eps >= 0. Sums are fp32. Tensors need only be aligned
+ * to their elements; where D is a multiple of 8 and they are 16-byte aligned,
+ * rows are moved with wide loads. */
+typedef enum { GDN2_NORM_LAYER = 0, GDN2_NORM_RMS = 1 } gdn2_norm_kind;
+
+typedef struct {
+  int64_t rows;
+  int32_t D;
+  int32_t kind;   /* a gdn2_norm_kind */
+  int32_t dtype;  /* a gdn2_dtype: x, gate, y and their gradients */
+  int32_t wdtype; /* a gdn2_dtype: weight, bias and their gradients */
+  float eps;
+} gdn2_norm_desc;
+
+/* y must not overlap an input (GDN2_ERR_ALIAS). */
+gdn2_status gdn2_norm_forward(const gdn2_norm_desc *desc, const void *x, const void *weight, const void *bias,
+                              const void *gate, void *y, void *stream);
+
+/* Gradients of gdn2_norm_forward, given dy ([rows, D], desc->dtype); the
+ * statistics are computed again from x.
+ *   dx : [rows, D].  dgate : [rows, D], or NULL (required NULL without a gate).
+ *   dweight, dbias : [D] in wdtype, summed over the rows in fp32 and in a fixed
+ *       order, or NULL (required NULL without a weight or bias). rows == 0
+ *       gives zeros.
+ * workspace: gdn2_norm_backward_workspace_bytes(desc) bytes, 16-byte aligned:
+ * partial sums of the weight's and the bias's gradient. */
+size_t gdn2_norm_backward_workspace_bytes(const gdn2_norm_desc *desc);
+gdn2_status gdn2_norm_backward(const gdn2_norm_desc *desc, const void *x, const void *weight, const void *bias,
+                               const void *gate, const void *dy, void *dx, void *dweight, void *dbias, void *dgate,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A cache of recurrent states in 8 bits (states kept for prompt prefixes, for
+ * paused requests): a quarter of the fp32 bytes. A state is `rows` rows of
+ * d_v values (the delta rule: rows = H_v * d_k; the linear recurrence's h of D
+ * channels: D / d_v rows). A row shares one power-of-two scale 2^e, the
+ * smallest (e >= -126) that keeps its largest magnitude within the format's
+ * largest value, so the one rounding is to the format's grid (half to even; no
+ * value rounds past the largest fp32 number):
+ *   GDN2_CACHE_E4M3 : 8-bit floating point, 4 exponent and 3 fraction bits,
+ *                     largest 448 (error at most 2^-4 of a value, or 2^-10
+ *                     scales below 2^-6 scales)
+ *   GDN2_CACHE_INT8 : whole numbers -127 .. 127 (error at most half a scale)
+ *   S      : [N, rows, d_v] fp32        slots : [N] int32 (device)
+ *   cache  : [P, rows, d_v] bytes       scales : [P, rows] bytes, e + 127
+ * d_v in {16, 32, 64, 128} (GDN2_ERR_UNSUPPORTED otherwise). S and cache
+ * 16-byte aligned, slots 4-byte. A row that holds an infinity or NaN gets the
+ * scale byte 255 and reads back as NaN; a scale byte of 0 (a cleared cache)
+ * reads back as zero. */
+typedef enum { GDN2_CACHE_E4M3 = 0, GDN2_CACHE_INT8 = 1 } gdn2_cache_format;
+
+typedef struct {
+  int32_t N, P;      /* entries of the call, slots of the cache */
+  int32_t rows, d_v; /* rows of a state, values of a row */
+  int32_t format;    /* a gdn2_cache_format */
+} gdn2_cache_desc;
+
+/* Entry n's state into slot slots[n]. A slot outside [0, P) is skipped; of
+ * entries that name the same slot the last one is kept. Slots that no entry
+ * names are left as they were. */
+gdn2_status gdn2_state_cache_store(const gdn2_cache_desc *desc, const float *S, const int32_t *slots, void *cache,
+                                   void *scales, void *stream);
+
+/* Slot slots[n]'s state into entry n. A slot outside [0, P) means no saved
+ * state: zeros. */
+gdn2_status gdn2_state_cache_load(const gdn2_cache_desc *desc, const void *cache, const void *scales,
+                                  const int32_t *slots, float *S, void *stream);
+
 /* Static, human-readable text for a status code. */
 const char *gdn2_status_string(gdn2_status status);
 
