@@ -22,39 +22,64 @@ namespace {
 
 constexpr int kNT = 256;
 
-template <class T, int N> struct alignas(sizeof(T) * N) Vec { T e[N]; };
+// N channels of a tensor as they lie in memory.
+template <bool BF16, int N> struct Raw;
+template <> struct Raw<false, 4> {
+  floatx4 v;
+  __device__ __forceinline__ float operator[](int c) const { return v[c]; }
+};
+template <> struct Raw<true, 4> {
+  typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
+  uintx2 v;
+  __device__ __forceinline__ float operator[](int c) const {
+    return __uint_as_float(c & 1 ? v[c >> 1] & 0xffff0000u : v[c >> 1] << 16);
+  }
+};
+template <> struct Raw<false, 1> {
+  float v;
+  __device__ __forceinline__ float operator[](int) const { return v; }
+};
+template <> struct Raw<true, 1> {
+  uint16_t v;
+  __device__ __forceinline__ float operator[](int) const { return bf16_to_f32(v); }
+};
+
+// Token tensors are read once, with nontemporal loads: a pass over the bytes
+// of the forward with its tiles' pattern ran at 6.16 TB/s with them and at
+// 5.23 TB/s without (bf16, 32768 x 2048).
+template <bool BF16, int N> __device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, size_t i) {
+  using T = typename Elem<BF16>::T;
+  using V = decltype(Raw<BF16, N>::v);
+  return Raw<BF16, N>{__builtin_nontemporal_load(reinterpret_cast<const V *>(static_cast<const T *>(p) + i))};
+}
 
 template <bool BF16, int N>
 __device__ __forceinline__ void load_f(float (&f)[N], const void *p, size_t i) {
   using T = typename Elem<BF16>::T;
-  const Vec<T, N> v = *reinterpret_cast<const Vec<T, N> *>(static_cast<const T *>(p) + i);
+  const Raw<BF16, N> r{*reinterpret_cast<const decltype(Raw<BF16, N>::v) *>(static_cast<const T *>(p) + i)};
 #pragma unroll
-  for (int c = 0; c < N; ++c) f[c] = Elem<BF16>::f(v.e[c]);
+  for (int c = 0; c < N; ++c) f[c] = r[c];
 }
 
 template <bool BF16, int N>
 __device__ __forceinline__ void store_f(void *p, size_t i, const float (&f)[N]) {
   using T = typename Elem<BF16>::T;
-  Vec<T, N> v;
+  struct alignas(sizeof(T) * N) { T e[N]; } v;
 #pragma unroll
   for (int c = 0; c < N; ++c) Elem<BF16>::st(&v.e[c], f[c]);
-  *reinterpret_cast<Vec<T, N> *>(static_cast<T *>(p) + i) = v;
-}
-
-// 1 / d for d >= 1 (v_rcp_f32 and one Newton step: within 1 ulp).
-__device__ __forceinline__ float recip(float d) {
-  const float r = __builtin_amdgcn_rcpf(d);
-  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  __builtin_memcpy(__builtin_assume_aligned(static_cast<T *>(p) + i, sizeof(T) * N), &v, sizeof(v));
 }
 
 // p = 1 / (1 + e^x) and q = 1 - p = e^x / (1 + e^x), neither by a difference:
-// both keep their relative accuracy however near the other is to 1. |x| above
-// 87 counts as 87, where e^x is still finite and p or q below 2e-38; NaN stays.
-__device__ __forceinline__ void split_sigmoid(float x, float &p, float &q) {
+// both keep their relative accuracy however near the other is to 1. x above
+// 87 counts as 87, where e^x is still finite and p 1.6e-38; NaN stays. EXACT
+// (fp32 pre-activations): the reciprocal's error of one step taken out by a
+// Newton step; a bf16 pre-activation is itself off by 2^-9 of its size.
+template <bool EXACT> __device__ __forceinline__ void split_sigmoid(float x, float &p, float &q) {
   x = x > 87.f ? 87.f : x;
-  x = x < -87.f ? -87.f : x;
-  const float e = __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
-  p = recip(1.f + e);
+  const float e = __builtin_amdgcn_exp2f(x * 1.44269504088896341f), d = 1.f + e;
+  p = __builtin_amdgcn_rcpf(d);
+  if constexpr (EXACT) p = __builtin_fmaf(__builtin_fmaf(-d, p, 1.f), p, p);
   q = e * p;
 }
 
@@ -63,24 +88,60 @@ template <int FORM> struct Form {
   static constexpr bool tied = FORM == GDN2_LINEAR_TIED || FORM == GDN2_LINEAR_TIED_PREACT;
 };
 
-// The gates of one token from what was loaded for them: decay a, input gate b.
-template <int FORM, int N>
-__device__ __forceinline__ void activate(float (&a)[N], float (&b)[N]) {
-#pragma unroll
-  for (int c = 0; c < N; ++c) {
-    if constexpr (Form<FORM>::pre) {
-      float q;
-      split_sigmoid(a[c], a[c], q);
-      if constexpr (Form<FORM>::tied) {
-        b[c] = q;
-      } else {
-        split_sigmoid(-b[c], b[c], q);
-      }
-    } else if constexpr (Form<FORM>::tied) {
-      b[c] = 1.f - a[c];
-    }
+// The gates of a value: decay a, input gate b.
+template <int FORM, bool EXACT> __device__ __forceinline__ void activate(float &a, float &b) {
+  if constexpr (Form<FORM>::pre) {
+    float q;
+    split_sigmoid<EXACT>(a, a, q);
+    if constexpr (Form<FORM>::tied)
+      b = q;
+    else
+      split_sigmoid<EXACT>(-b, b, q);
+  } else if constexpr (Form<FORM>::tied) {
+    b = 1.f - a;
   }
 }
+
+// A sigmoid and its complement in one word: the smaller of the two, the
+// complement with its sign set. Both come back without a difference that
+// loses digits, which the gradient through the activation, p (1 - p), needs.
+__device__ __forceinline__ float pack_pair(float p, float q) { return p <= q ? p : -q; }
+__device__ __forceinline__ void unpack_pair(float v, float &p, float &q) {
+  const float o = 1.f - __builtin_fabsf(v);
+  p = v > 0.f ? v : o;
+  q = v > 0.f ? o : -v;
+}
+
+// A token's gates as the backward keeps them (one word each) and its
+// gradients from them.
+template <int FORM, bool EXACT> struct Gates {
+  static __device__ __forceinline__ void pack(float &a, float &b) {
+    if constexpr (Form<FORM>::pre) {
+      float p, q;
+      split_sigmoid<EXACT>(a, p, q);
+      a = pack_pair(p, q);
+      if constexpr (!Form<FORM>::tied) {
+        split_sigmoid<EXACT>(-b, p, q);
+        b = pack_pair(p, q);
+      }
+    }
+  }
+  // a, 1 - a, b, 1 - b (the complements in the pre-activation forms only)
+  static __device__ __forceinline__ void unpack(float va, float vb, float &a, float &na, float &b, float &nb) {
+    if constexpr (Form<FORM>::pre) {
+      unpack_pair(va, a, na);
+      if constexpr (Form<FORM>::tied)
+        b = na;
+      else
+        unpack_pair(vb, b, nb);
+    } else {
+      a = va;
+      b = Form<FORM>::tied ? 1.f - va : vb;
+    }
+  }
+  static constexpr float kNone = -0.f;  // va of a token that passes the state on: a = 1
+  static __device__ __forceinline__ float none() { return Form<FORM>::pre ? kNone : 1.f; }
+};
 
 struct Lin {
   const void *x, *a, *b;
@@ -102,10 +163,26 @@ template <int VEC> struct Geo {
   static constexpr int CT = kLinChannels / VEC, NS = kNT / CT, L = kLinTile / NS, WS = 64 / CT;  // WS: slots a wave
 };
 
+// (A, U) := (a, u) after (A, U). CUT: a map with A = 0 takes nothing from what
+// lies before it, not even a NaN or an infinity: that is how a sequence of a
+// packed batch starts (below).
+template <bool CUT> __device__ __forceinline__ void after(float a, float u, float &A, float &U) {
+  if (CUT && a == 0.f) {
+    A = 0.f;
+    U = u;
+  } else {
+    U = __builtin_fmaf(a, U, u);
+    A *= a;
+  }
+}
+template <bool CUT> __device__ __forceinline__ float apply(float a, float u, float h) {
+  return CUT && a == 0.f ? u : __builtin_fmaf(a, h, u);
+}
+
 // Scan of the threads' maps (A, U) in token order (or, REV, from the last
 // token to the first): on return (A, U) is the map of all earlier threads of
 // this wave, and tot[w] in LDS the whole map of wave w.
-template <int VEC, bool REV>
+template <int VEC, bool REV, bool CUT>
 __device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&U)[VEC], float2 (*tot)[kLinChannels], int tid) {
   using G = Geo<VEC>;
   const int lane = tid & 63, w = tid >> 6, ct = lane % G::CT, sl = lane / G::CT;
@@ -117,8 +194,8 @@ __device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&U)[VEC], floa
       const float pa = REV ? __shfl_down(A[c], off * G::CT, 64) : __shfl_up(A[c], off * G::CT, 64);
       const float pu = REV ? __shfl_down(U[c], off * G::CT, 64) : __shfl_up(U[c], off * G::CT, 64);
       if (has) {
-        U[c] = __builtin_fmaf(A[c], pu, U[c]);
-        A[c] *= pa;
+        U[c] = apply<CUT>(A[c], U[c], pu);
+        A[c] = CUT && A[c] == 0.f ? 0.f : A[c] * pa;
       }
     }
   }
@@ -143,7 +220,7 @@ __device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&U)[VEC], floa
 
 // The value entering this thread's tokens and the value leaving the tile,
 // from the value entering the tile (carry, replaced by the leaving one).
-template <int VEC, bool REV>
+template <int VEC, bool REV, bool CUT>
 __device__ __forceinline__ void enter(float (&in)[VEC], float (&carry)[VEC], const float (&A)[VEC],
                                       const float (&U)[VEC], const float2 (*tot)[kLinChannels], int tid) {
   using G = Geo<VEC>;
@@ -156,210 +233,435 @@ __device__ __forceinline__ void enter(float (&in)[VEC], float (&carry)[VEC], con
       const int j = REV ? 3 - i : i;
       if (j == w) mine = h;
       const float2 t = tot[j][ct * VEC + c];
-      h = __builtin_fmaf(t.x, h, t.y);
+      h = apply<CUT>(t.x, t.y, h);
     }
-    in[c] = __builtin_fmaf(A[c], mine, U[c]);
+    in[c] = apply<CUT>(A[c], U[c], mine);
     carry[c] = h;
   }
 }
 
-// One workgroup per (sequence, 64 channels), tile after tile. Tiles lie on
-// multiples of 128 of the token axis (packed sequences: of the packed axis),
-// so that the saved states' rows are the same whatever the sequences.
-template <bool BF16, int FORM, int VEC>
-__global__ __launch_bounds__(kNT) void linear_forward_seq(Lin p) {
-  using G = Geo<VEC>;
-  constexpr bool GB = BF16 && Form<FORM>::pre;  // gates in bf16
-  __shared__ float2 tot[2][4][kLinChannels];
-  const int tid = threadIdx.x, ct = tid % G::CT, s = tid / G::CT;
-  const int n = blockIdx.x / p.nblk, blk = blockIdx.x - n * p.nblk;
-  const int D = p.D, c0 = blk * kLinChannels + ct * VEC;
-  const bool own = c0 < D;
-  const int cc = own ? c0 : D - VEC;  // a channel to read in any case
-  int lo = 0, hi = p.T;
-  size_t row0 = (size_t)n * p.T;
-  if (p.cu) {
-    lo = clamp_offset(p.cu[n], p.T);
-    hi = clamp_offset(p.cu[n + 1], p.T);
-    row0 = 0;
-  }
-  const size_t ck0 = p.cu ? 0 : (size_t)n * ((p.T + kLinTile - 1) / kLinTile);
-  float carry[VEC];
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) carry[c] = p.h0 ? p.h0[(size_t)n * D + cc + c] : 0.f;
-  int par = 0;
-  for (int t0 = hi > lo ? lo - lo % kLinTile : hi; t0 < hi; t0 += kLinTile, par ^= 1) {
-    if (p.ck && own && s == 0 && t0 > lo) store_f<false>(p.ck, (ck0 + t0 / kLinTile) * D + c0, carry);
-    float a[G::L][VEC], u[G::L][VEC];
-    const int ts = t0 + s * G::L;
-#pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-      const int t = ts + i, tc = t < lo ? lo : t >= hi ? hi - 1 : t;
-      const size_t at = (row0 + tc) * D + cc;
-      float b[VEC];
-      load_f<BF16>(u[i], p.x, at);
-      load_f<GB>(a[i], p.a, at);
-      if constexpr (!Form<FORM>::tied) load_f<GB>(b, p.b, at);
-      activate<FORM>(a[i], b);
-      const bool in = t == tc;  // outside the sequence: the identity map
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        u[i][c] = in ? b[c] * u[i][c] : 0.f;
-        a[i][c] = in ? a[i][c] : 1.f;
-      }
-    }
-    float A[VEC], U[VEC], h[VEC];
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      A[c] = a[0][c];
-      U[c] = u[0][c];
-    }
-#pragma unroll
-    for (int i = 1; i < G::L; ++i) {
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        U[c] = __builtin_fmaf(a[i][c], U[c], u[i][c]);
-        A[c] *= a[i][c];
-      }
-    }
-    wave_scan<VEC, false>(A, U, tot[par], tid);
+// ------------------------------------------------------------------ tiles in parallel
+// The tiles of one chain (a sequence's, or the packed axis', and 64 channels)
+// run at once, each read from memory once. A workgroup takes its chain's next
+// tile by a ticket, so that every tile it waits for was taken before it and is
+// running or done: no wait is endless. (A ticket per chain: one counter for all
+// of them hands out a tile every 15 ns, which bound the whole kernel.) It publishes its tile's map, and finds
+// the value entering the tile from
+//   the maps of the tiles before it in its group of kGroup tiles, composed,
+//   applied to the value that left the group before (published by that
+//   group's last tile): the same sums in the same order whatever the timing.
+// Each published word validates itself (a map's two floats in 64 bits, a
+// value in 32; all bits set: not there yet; NaN published as the quiet NaN),
+// so relaxed agent-scope accesses suffice: no fence writes a cache back.
+constexpr int kGroup = 16;
+constexpr int kTicketWords = 16;
+constexpr int kSpins = 1 << 24;  // a wait given up after this many looks yields NaN
+
+struct Chain {
+  uint32_t *ticket;  // [chain], kTicketWords apart
+  uint64_t *map;    // [tile][chain][64]
+  uint32_t *value;  // [group][chain][64]
+  int chains, tiles;
+};
+
+__device__ __forceinline__ uint32_t word(float f) { return f != f ? 0x7fc00000u : __float_as_uint(f); }
+
+// Tile of this workgroup: its index k along the walk and its chain.
+__device__ __forceinline__ void take_tile(const Chain &ch, int *slot, int tid, int &k, int &chain) {
+  chain = blockIdx.x % ch.chains;
+  k = 0;
+  if (ch.tiles > 1) {
+    if (tid == 0)  // the tickets start at 2^32 - 1
+      *slot = (int)(__hip_atomic_fetch_add(ch.ticket + (size_t)chain * kTicketWords, 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT) + 1u);
     __syncthreads();
-    enter<VEC, false>(h, carry, A, U, tot[par], tid);
-    if (p.o) {
-#pragma unroll
-      for (int i = 0; i < G::L; ++i) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) h[c] = __builtin_fmaf(a[i][c], h[c], u[i][c]);
-        const int t = ts + i;
-        if (own && t >= lo && t < hi) store_f<BF16>(p.o, (row0 + t) * D + c0, h);
-      }
-    }
+    k = __builtin_amdgcn_readfirstlane(*slot);
   }
-  if (p.h_T && own && s == 0) store_f<false>(p.h_T, (size_t)n * D + c0, carry);
 }
 
-// Gradients. With m the adjoint of the state between two tokens (dh_T after
-// the last one), token t takes g = dO_t + m_{t+1} and gives
-//   dx = b g,  db = x g,  da = g h_{t-1},  m_t = a g,
-// so that m runs through the maps (a, a dO) from the last token to the first,
-// and h_{t-1} is walked again from the state saved at the tile's first token.
-template <bool BF16, int FORM, int VEC>
-__global__ __launch_bounds__(kNT) void linear_backward_seq(Lin p) {
+// The value entering tile k of its chain, for this lane's channel in wave 0
+// (start: the value entering the chain), from the tiles' published maps; own:
+// this tile's map. Publishes both. Every thread of the workgroup calls it.
+template <bool CUT>
+__device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 own, float start,
+                                      float2 (*maps)[kLinChannels], int tid) {
+  const int lane = tid & 63, w = tid >> 6, in = k % kGroup;
+  if (ch.tiles == 1) return start;
+  if (w == 0 && in != kGroup - 1 && k != ch.tiles - 1)
+    __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * 64 + lane,
+                       (uint64_t)word(own.x) | (uint64_t)word(own.y) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  uint64_t v[kGroup / 4];
+  const uint64_t *at = ch.map + ((size_t)(k - in + w) * ch.chains + chain) * 64 + lane;
+  for (int spin = 0; spin < kSpins; ++spin) {
+    bool ready = true;
+#pragma unroll
+    for (int j = 0; j < kGroup / 4; ++j) {
+      v[j] = 0;
+      if (4 * j + w < in)
+        v[j] = __hip_atomic_load(at + (size_t)4 * j * ch.chains * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      ready = ready && v[j] != ~(uint64_t)0;
+    }
+    if (ready) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
+#pragma unroll
+  for (int j = 0; j < kGroup / 4; ++j)
+    maps[4 * j + w][lane] = float2{__uint_as_float((uint32_t)v[j]), __uint_as_float((uint32_t)(v[j] >> 32))};
+  __syncthreads();
+  if (w != 0) return 0.f;
+  float A = 1.f, U = 0.f;
+  for (int j = 0; j < in; ++j) after<CUT>(maps[j][lane].x, maps[j][lane].y, A, U);
+  float h = start;
+  if (k >= kGroup) {
+    uint32_t p = ~0u;
+    const uint32_t *q = ch.value + ((size_t)(k / kGroup - 1) * ch.chains + chain) * 64 + lane;
+    for (int spin = 0; spin < kSpins; ++spin) {
+      p = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (p != ~0u) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+    h = __uint_as_float(p);  // all bits set is a NaN
+  }
+  h = apply<CUT>(A, U, h);
+  if (in == kGroup - 1 && k != ch.tiles - 1)
+    __hip_atomic_store(ch.value + ((size_t)(k / kGroup) * ch.chains + chain) * 64 + lane, word(apply<CUT>(own.x, own.y, h)),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return h;
+}
+
+// A tile's map from its waves', for this lane's channel.
+template <bool REV, bool CUT> __device__ __forceinline__ float2 tile_map(const float2 (*tot)[kLinChannels], int lane) {
+  float A = 1.f, U = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = tot[REV ? 3 - i : i][lane];
+    after<CUT>(t.x, t.y, A, U);
+  }
+  return float2{A, U};
+}
+
+// Which sequence starts and which ends at each token of a packed tile (-1: none).
+struct Edges {
+  int start[kLinTile], end[kLinTile];
+};
+
+__device__ __forceinline__ void find_edges(Edges &e, const Lin &p, int t0, int tid) {
+  if (tid < kLinTile) e.start[tid] = -1;
+  else e.end[tid - kLinTile] = -1;
+  // the first sequence that may reach into the tile, to within 256
+  int lo = 0, hi = p.B;
+  while (hi - lo > kNT) {
+    const int mid = lo + (hi - lo) / 2;
+    if (clamp_offset(p.cu[mid], p.T) <= t0) lo = mid;
+    else hi = mid;
+  }
+  __syncthreads();
+  for (int n = lo + tid; n < p.B; n += kNT) {
+    const int b = clamp_offset(p.cu[n], p.T), f = clamp_offset(p.cu[n + 1], p.T);
+    if (b >= t0 + kLinTile) break;
+    if (b >= f) continue;
+    if (b >= t0) e.start[b - t0] = n;
+    if (f > t0 && f <= t0 + kLinTile) e.end[f - 1 - t0] = n;
+  }
+  __syncthreads();
+}
+
+template <bool BF16, int FORM, int VEC, bool PACKED>
+__global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  __shared__ float2 tot[2][2][4][kLinChannels];
-  const int tid = threadIdx.x, ct = tid % G::CT, s = tid / G::CT;
-  const int n = blockIdx.x / p.nblk, blk = blockIdx.x - n * p.nblk;
+  __shared__ float2 tot[4][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float entering[kLinChannels];
+  __shared__ Edges edges[1];
+  __shared__ int slot;
+  const int tid = threadIdx.x, lane = tid & 63, ct = tid % G::CT, s = tid / G::CT;
+  int k, chain;
+  take_tile(ch, &slot, tid, k, chain);
+  const int n = PACKED ? 0 : chain / p.nblk, blk = chain - n * p.nblk;
   const int D = p.D, c0 = blk * kLinChannels + ct * VEC;
   const bool own = c0 < D;
-  const int cc = own ? c0 : D - VEC;
+  const int cc = own ? c0 : D - VEC, t0 = k * kLinTile, ts = t0 + s * G::L;
   int lo = 0, hi = p.T;
-  size_t row0 = (size_t)n * p.T;
-  if (p.cu) {
-    lo = clamp_offset(p.cu[n], p.T);
-    hi = clamp_offset(p.cu[n + 1], p.T);
-    row0 = 0;
+  if constexpr (PACKED) {
+    lo = clamp_offset(p.cu[0], p.T);
+    hi = clamp_offset(p.cu[p.B], p.T);
   }
-  const size_t ck0 = p.cu ? 0 : (size_t)n * ((p.T + kLinTile - 1) / kLinTile);
-  float m[VEC];
+  const size_t row0 = PACKED ? 0 : (size_t)n * p.T, ck0 = PACKED ? 0 : (size_t)n * ch.tiles;
+
+  Raw<BF16, VEC> xr[G::L];
+  Raw<GB, VEC> ar[G::L], br[G::L];
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) m[c] = p.dh_T ? p.dh_T[(size_t)n * D + cc + c] : 0.f;
-  int par = 0;
-  const int first = lo - lo % kLinTile;
-  for (int t0 = hi > lo ? (hi - 1) - (hi - 1) % kLinTile : first - kLinTile; t0 >= first; t0 -= kLinTile, par ^= 1) {
-    float hin[VEC];
+  for (int i = 0; i < G::L; ++i) {
+    const int t = ts + i;
+    const size_t at = (row0 + (t < p.T ? t : p.T - 1)) * D + cc;
+    xr[i] = load_raw<BF16, VEC>(p.x, at);
+    ar[i] = load_raw<GB, VEC>(p.a, at);
+    if constexpr (!Form<FORM>::tied) br[i] = load_raw<GB, VEC>(p.b, at);
+  }
+  if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
+  float a[G::L][VEC], u[G::L][VEC];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c)
-      hin[c] = t0 > lo ? p.ck[(ck0 + t0 / kLinTile) * D + cc + c] : p.h0 ? p.h0[(size_t)n * D + cc + c] : 0.f;
-    float a[G::L][VEC], x[G::L][VEC], b[G::L][VEC], dO[G::L][VEC];
-    const int ts = t0 + s * G::L;
-#pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-      const int t = ts + i, tc = t < lo ? lo : t >= hi ? hi - 1 : t;
-      const size_t at = (row0 + tc) * D + cc;
-      load_f<BF16>(x[i], p.x, at);
-      load_f<GB>(a[i], p.a, at);
-      if constexpr (!Form<FORM>::tied) load_f<GB>(b[i], p.b, at);
-      load_f<BF16>(dO[i], p.dO, at);
-      activate<FORM>(a[i], b[i]);
-      if (t != tc) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          a[i][c] = 1.f;
-          b[i][c] = x[i][c] = dO[i][c] = 0.f;
-        }
-      }
-    }
-    float A[VEC], U[VEC], Am[VEC], Um[VEC], h[VEC], mi[VEC];
+  for (int i = 0; i < G::L; ++i) {
+    const int t = ts + i;
+    const bool in = t >= lo && t < hi;  // outside: the identity map
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      A[c] = 1.f;
-      U[c] = Um[c] = 0.f;
+      float av = ar[i][c], bv = 0.f;
+      if constexpr (!Form<FORM>::tied) bv = br[i][c];
+      activate<FORM, !BF16>(av, bv);
+      u[i][c] = in ? bv * xr[i][c] : 0.f;
+      a[i][c] = in ? av : 1.f;
     }
+    if constexpr (PACKED) {  // a sequence starts: its own state, and a cut
+      const int q = edges[0].start[s * G::L + i];
+      if (q >= 0) {
 #pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        U[c] = __builtin_fmaf(a[i][c], U[c], b[i][c] * x[i][c]);
-        A[c] *= a[i][c];
-        const float *r = a[G::L - 1 - i], *d = dO[G::L - 1 - i];
-        Um[c] = r[c] * (d[c] + Um[c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) Am[c] = A[c];
-    wave_scan<VEC, false>(A, U, tot[par][0], tid);
-    wave_scan<VEC, true>(Am, Um, tot[par][1], tid);
-    __syncthreads();
-    enter<VEC, false>(h, hin, A, U, tot[par][0], tid);
-    enter<VEC, true>(mi, m, Am, Um, tot[par][1], tid);
-    float hp[G::L][VEC];
-#pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        hp[i][c] = h[c];
-        h[c] = __builtin_fmaf(a[i][c], h[c], b[i][c] * x[i][c]);
-      }
-    }
-#pragma unroll
-    for (int i = G::L - 1; i >= 0; --i) {
-      const int t = ts + i;
-      float dx[VEC], da[VEC], db[VEC];
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) {
-        const float g = dO[i][c] + mi[c];
-        mi[c] = a[i][c] * g;
-        dx[c] = b[i][c] * g;
-        db[c] = x[i][c] * g;
-        da[c] = Form<FORM>::tied ? g * (hp[i][c] - x[i][c]) : g * hp[i][c];
-      }
-      if (own && t >= lo && t < hi) {
-        const size_t at = (row0 + t) * D + c0;
-        if constexpr (Form<FORM>::pre) {
-          // through the activations: a' = -a (1 - a), b' = b (1 - b), the
-          // complements again without a difference
-          float pa[VEC], pb[VEC];
-          load_f<GB>(pa, p.a, at);
-          if constexpr (!Form<FORM>::tied) load_f<GB>(pb, p.b, at);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            float y, z;
-            split_sigmoid(pa[c], y, z);
-            da[c] *= -y * z;
-            if constexpr (!Form<FORM>::tied) {
-              split_sigmoid(pb[c], y, z);
-              db[c] *= y * z;
-            }
-          }
+        for (int c = 0; c < VEC; ++c) {
+          if (p.h0) u[i][c] = __builtin_fmaf(a[i][c], p.h0[(size_t)q * D + cc + c], u[i][c]);
+          a[i][c] = 0.f;
         }
-        store_f<BF16>(p.dx, at, dx);
-        store_f<GB>(p.da, at, da);
-        if constexpr (!Form<FORM>::tied) store_f<GB>(p.db, at, db);
       }
     }
   }
-  if (p.dh0 && own && s == 0) store_f<false>(p.dh0, (size_t)n * D + c0, m);
+  float A[VEC], U[VEC], h[VEC], carry[VEC];
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) {
+    A[c] = a[0][c];
+    U[c] = u[0][c];
+  }
+#pragma unroll
+  for (int i = 1; i < G::L; ++i) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) after<PACKED>(a[i][c], u[i][c], A[c], U[c]);
+  }
+  wave_scan<VEC, false, PACKED>(A, U, tot, tid);
+  __syncthreads();
+  {
+    const int c = blk * kLinChannels + lane;
+    const float start = !PACKED && p.h0 && c < D && tid < 64 ? p.h0[(size_t)n * D + c] : 0.f;
+    const float in = link<PACKED>(ch, k, chain, tile_map<false, PACKED>(tot, lane), start, maps, tid);
+    if (tid < 64) {
+      entering[lane] = in;
+      if (p.ck && k > 0 && c < D) p.ck[(ck0 + k) * D + c] = in;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) carry[c] = entering[ct * VEC + c];
+  enter<VEC, false, PACKED>(h, carry, A, U, tot, tid);
+#pragma unroll
+  for (int i = 0; i < G::L; ++i) {
+    const int t = ts + i;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = apply<PACKED>(a[i][c], u[i][c], h[c]);
+    if (own && t >= lo && t < hi) {
+      if (p.o) store_f<BF16>(p.o, (row0 + t) * D + c0, h);
+      if constexpr (PACKED) {
+        const int q = edges[0].end[s * G::L + i];
+        if (q >= 0 && p.h_T) store_f<false>(p.h_T, (size_t)q * D + c0, h);
+      }
+    }
+  }
+  if (!PACKED && p.h_T && k == ch.tiles - 1 && own && s == 0) store_f<false>(p.h_T, (size_t)n * D + c0, carry);
+}
+
+// The gradients, tile by tile from the last one: the adjoint is chained, the
+// states come from the saved ones.
+template <bool BF16, int FORM, int VEC, bool PACKED>
+__global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
+  using G = Geo<VEC>;
+  constexpr bool GB = BF16 && Form<FORM>::pre;
+  __shared__ float2 tot[2][4][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float entering[kLinChannels];
+  __shared__ Edges edges[1];
+  __shared__ int slot;
+  const int tid = threadIdx.x, lane = tid & 63, ct = tid % G::CT, s = tid / G::CT;
+  int k, chain;
+  take_tile(ch, &slot, tid, k, chain);
+  const int n = PACKED ? 0 : chain / p.nblk, blk = chain - n * p.nblk;
+  const int D = p.D, c0 = blk * kLinChannels + ct * VEC;
+  const bool own = c0 < D;
+  const int tile = ch.tiles - 1 - k;
+  const int cc = own ? c0 : D - VEC, t0 = tile * kLinTile, ts = t0 + s * G::L;
+  int lo = 0, hi = p.T;
+  if constexpr (PACKED) {
+    lo = clamp_offset(p.cu[0], p.T);
+    hi = clamp_offset(p.cu[p.B], p.T);
+  }
+  const size_t row0 = PACKED ? 0 : (size_t)n * p.T, ck0 = PACKED ? 0 : (size_t)n * ch.tiles;
+
+  using GT = Gates<FORM, !BF16>;
+  Raw<BF16, VEC> x[G::L], dr[G::L];
+  float va[G::L][VEC], vb[G::L][VEC], hin[VEC];
+  {
+    Raw<GB, VEC> ar[G::L], br[G::L];
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      const int t = ts + i;
+      const size_t at = (row0 + (t < p.T ? t : p.T - 1)) * D + cc;
+      x[i] = load_raw<BF16, VEC>(p.x, at);
+      ar[i] = load_raw<GB, VEC>(p.a, at);
+      if constexpr (!Form<FORM>::tied) br[i] = load_raw<GB, VEC>(p.b, at);
+      dr[i] = load_raw<BF16, VEC>(p.dO, at);
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c)
+      hin[c] = tile > 0 ? p.ck[(ck0 + tile) * D + cc + c] : !PACKED && p.h0 ? p.h0[(size_t)n * D + cc + c] : 0.f;
+    if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      const bool in = ts + i >= lo && ts + i < hi;
+      if (!in) x[i].v = dr[i].v = decltype(x[i].v){};
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        va[i][c] = ar[i][c];
+        vb[i][c] = 0.f;
+        if constexpr (!Form<FORM>::tied) vb[i][c] = br[i][c];
+        GT::pack(va[i][c], vb[i][c]);
+        va[i][c] = in ? va[i][c] : GT::none();
+        vb[i][c] = in ? vb[i][c] : 0.f;
+      }
+    }
+  }
+  // the outputs' gradients; a packed sequence's last token adds its state's,
+  // read before anything is published (dh0 may be dh_T)
+  float dE[PACKED ? G::L : 1][VEC];
+  if constexpr (PACKED) {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      const int q = edges[0].end[s * G::L + i];
+#pragma unroll
+      for (int c = 0; c < VEC; ++c)
+        dE[i][c] = dr[i][c] + (q >= 0 && p.dh_T ? p.dh_T[(size_t)q * D + cc + c] : 0.f);
+    }
+  }
+  // between the passes over the tokens: what is unpacked for one pass is not
+  // kept for the next (256 + 97 registers otherwise, bf16 pre-activations)
+  auto hold = [&] {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      pin_regs(va[i]);
+      if constexpr (!Form<FORM>::tied) pin_regs(vb[i]);
+      if constexpr (sizeof(x[i]) % 4 == 0) {
+        pin_regs(x[i].v);
+        if constexpr (!PACKED) pin_regs(dr[i].v);
+      }
+    }
+  };
+  auto dO = [&](int i, int c) { return PACKED ? dE[PACKED ? i : 0][c] : dr[i][c]; };
+  float A[VEC], U[VEC], Am[VEC], Um[VEC], h[VEC], mi[VEC], m[VEC];
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) {
+    A[c] = Am[c] = 1.f;
+    U[c] = Um[c] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < G::L; ++i) {
+    const int j = G::L - 1 - i;
+    const int q = PACKED ? edges[0].start[s * G::L + i] : -1;
+    const bool cut = PACKED && edges[0].end[s * G::L + j] >= 0;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      float a, na, b, nb, am, x0, x1, x2;
+      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
+      GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
+      const float u = b * x[i][c];
+      if constexpr (PACKED) {
+        if (q >= 0)
+          after<true>(0.f, p.h0 ? __builtin_fmaf(a, p.h0[(size_t)q * D + cc + c], u) : u, A[c], U[c]);
+        else
+          after<true>(a, u, A[c], U[c]);
+        after<true>(cut ? 0.f : am, am * dO(j, c), Am[c], Um[c]);
+      } else {
+        U[c] = __builtin_fmaf(a, U[c], u);
+        A[c] *= a;
+        Um[c] = am * (dO(j, c) + Um[c]);
+        Am[c] = A[c];
+      }
+    }
+  }
+  hold();
+  wave_scan<VEC, false, PACKED>(A, U, tot[0], tid);
+  wave_scan<VEC, true, PACKED>(Am, Um, tot[1], tid);
+  __syncthreads();
+  {
+    const int c = blk * kLinChannels + lane;
+    const float start = !PACKED && p.dh_T && c < D && tid < 64 ? p.dh_T[(size_t)n * D + c] : 0.f;
+    const float in = link<PACKED>(ch, k, chain, tile_map<true, PACKED>(tot[1], lane), start, maps, tid);
+    if (tid < 64) entering[lane] = in;
+  }
+  enter<VEC, false, PACKED>(h, hin, A, U, tot[0], tid);
+  float hp[G::L][VEC];
+#pragma unroll
+  for (int i = 0; i < G::L; ++i) {
+    if constexpr (PACKED) {
+      const int q = edges[0].start[s * G::L + i];
+      if (q >= 0) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h[c] = p.h0 ? p.h0[(size_t)q * D + cc + c] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      float a, na, b, nb;
+      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
+      hp[i][c] = h[c];
+      h[c] = __builtin_fmaf(a, h[c], b * x[i][c]);
+    }
+  }
+  hold();
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) m[c] = entering[ct * VEC + c];
+  enter<VEC, true, PACKED>(mi, m, Am, Um, tot[1], tid);
+#pragma unroll
+  for (int i = G::L - 1; i >= 0; --i) {
+    const int t = ts + i;
+    float dx[VEC], da[VEC], db[VEC];
+    const bool cut = PACKED && edges[0].end[s * G::L + i] >= 0;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      float a, na, b, nb;
+      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
+      const float g = dO(i, c) + (cut ? 0.f : mi[c]), xv = x[i][c];
+      mi[c] = a * g;
+      dx[c] = b * g;
+      db[c] = xv * g;
+      da[c] = Form<FORM>::tied ? g * (hp[i][c] - xv) : g * hp[i][c];
+      if constexpr (Form<FORM>::pre) {  // through the activations: a' = -a (1 - a), b' = b (1 - b)
+        da[c] *= -a * na;
+        if constexpr (!Form<FORM>::tied) db[c] *= b * nb;
+      }
+    }
+    if (own && t < p.T) {
+      const size_t at = (row0 + t) * D + c0;
+      if (PACKED && (t < lo || t >= hi)) {  // no sequence's token: no gradient
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) dx[c] = da[c] = db[c] = 0.f;
+      }
+      store_f<BF16>(p.dx, at, dx);
+      store_f<GB>(p.da, at, da);
+      if constexpr (!Form<FORM>::tied) store_f<GB>(p.db, at, db);
+      if constexpr (PACKED) {
+        const int q = edges[0].start[s * G::L + i];
+        if (q >= 0 && p.dh0) store_f<false>(p.dh0, (size_t)q * D + c0, mi);
+      }
+    }
+  }
+  if (!PACKED && p.dh0 && tile == 0 && own && s == 0) store_f<false>(p.dh0, (size_t)n * D + c0, m);
+}
+
+// Before a chained launch: the words not published yet, and what needs no
+// token: the states of empty sequences pass through (all of them without cu).
+__global__ __launch_bounds__(kNT) void chain_prepare(uint4 *words, size_t count, const int32_t *cu, int B, int T, int D,
+                                                     const float *from, float *to) {
+  const size_t me = (size_t)blockIdx.x * kNT + threadIdx.x;
+  for (size_t i = me; i < count; i += (size_t)gridDim.x * kNT) words[i] = uint4{~0u, ~0u, ~0u, ~0u};
+  if (!to) return;
+  for (int n = blockIdx.x; n < B; n += gridDim.x) {
+    if (cu && clamp_offset(cu[n + 1], T) > clamp_offset(cu[n], T)) continue;
+    for (int c = threadIdx.x; c < D; c += kNT) to[(size_t)n * D + c] = from ? from[(size_t)n * D + c] : 0.f;
+  }
 }
 
 // One token: a thread per VEC channels of a row.
@@ -372,15 +674,23 @@ __global__ __launch_bounds__(kNT) void linear_step(Lin p, size_t total) {
     load_f<GB>(a, p.a, i);
     if constexpr (!Form<FORM>::tied) load_f<GB>(b, p.b, i);
     load_f<BF16>(x, p.x, i);
-    activate<FORM>(a, b);
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) h[c] = __builtin_fmaf(a[c], h[c], b[c] * x[c]);
+    for (int c = 0; c < VEC; ++c) {
+      activate<FORM, !BF16>(a[c], b[c]);
+      h[c] = __builtin_fmaf(a[c], h[c], b[c] * x[c]);
+    }
     store_f<false>(p.h_T, i, h);
     store_f<BF16>(p.o, i, h);
   }
 }
 
 enum Op { kForward, kBackward, kStep };
+
+// Bytes of a chained launch's words: the tickets, the maps, the values.
+size_t chain_bytes(int chains, int tiles) {
+  if (tiles <= 1) return 0;
+  return (size_t)chains * (kTicketWords * 4 + (size_t)tiles * 64 * 8 + (size_t)((tiles + kGroup - 1) / kGroup) * 64 * 4);
+}
 
 template <bool BF16, int FORM, int VEC>
 hipError_t launch_v(const LinearArgs &q, Op op, hipStream_t st) {
@@ -393,11 +703,34 @@ hipError_t launch_v(const LinearArgs &q, Op op, hipStream_t st) {
                        total);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((size_t)q.B * p.nblk));
-  if (op == kForward)
-    hipLaunchKernelGGL((linear_forward_seq<BF16, FORM, VEC>), grid, dim3(kNT), 0, st, p);
-  else
-    hipLaunchKernelGGL((linear_backward_seq<BF16, FORM, VEC>), grid, dim3(kNT), 0, st, p);
+  Chain ch{};
+  ch.chains = (q.cu ? 1 : q.B) * p.nblk;
+  ch.tiles = (q.T + kLinTile - 1) / kLinTile;
+  const size_t bytes = chain_bytes(ch.chains, ch.tiles);
+  if (bytes) {
+    ch.ticket = static_cast<uint32_t *>(q.workspace);
+    ch.map = reinterpret_cast<uint64_t *>(ch.ticket + (size_t)ch.chains * kTicketWords);
+    ch.value = reinterpret_cast<uint32_t *>(ch.map + (size_t)ch.tiles * ch.chains * 64);
+  }
+  const float *from = op == kForward ? q.h0 : q.dh_T;
+  float *to = !q.cu && ch.tiles ? nullptr : op == kForward ? q.h_T : q.dh0;
+  if (bytes || to) {
+    const size_t count = bytes / 16, wgs = (count + kNT - 1) / kNT;
+    const size_t grid = wgs < 1 ? 1 : wgs > 2048 ? 2048 : wgs;
+    hipLaunchKernelGGL(chain_prepare, dim3((unsigned)grid), dim3(kNT), 0, st, static_cast<uint4 *>(q.workspace), count, q.cu,
+                       q.B, q.T, q.D, from, to);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (ch.tiles == 0) return hipSuccess;
+  const dim3 grid((unsigned)((size_t)ch.chains * ch.tiles));
+  if (op == kForward) {
+    if (q.cu) hipLaunchKernelGGL((linear_forward_chain<BF16, FORM, VEC, true>), grid, dim3(kNT), 0, st, p, ch);
+    else hipLaunchKernelGGL((linear_forward_chain<BF16, FORM, VEC, false>), grid, dim3(kNT), 0, st, p, ch);
+  } else {
+    if (q.cu) hipLaunchKernelGGL((linear_backward_chain<BF16, FORM, VEC, true>), grid, dim3(kNT), 0, st, p, ch);
+    else hipLaunchKernelGGL((linear_backward_chain<BF16, FORM, VEC, false>), grid, dim3(kNT), 0, st, p, ch);
+  }
   return hipGetLastError();
 }
 
@@ -430,12 +763,16 @@ hipError_t launch(const LinearArgs &q, Op op, hipStream_t st) {
 
 }  // namespace
 
+size_t linear_chain_bytes(int B, int T, int D, bool packed) {
+  return chain_bytes((packed ? 1 : B) * ((D + kLinChannels - 1) / kLinChannels), (T + kLinTile - 1) / kLinTile);
+}
+
 hipError_t launch_linear_forward(const LinearArgs &q, hipStream_t st) { return launch(q, kForward, st); }
 
 hipError_t launch_linear_backward(const LinearArgs &q, hipStream_t st) {
   LinearArgs p = q;
   if (!p.ck) {  // the saved states again: a forward pass that writes nothing else
-    p.ck = static_cast<float *>(p.workspace);
+    p.ck = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + linear_chain_bytes(p.B, p.T, p.D, p.cu != nullptr));
     LinearArgs f = p;
     f.o = nullptr;
     f.h_T = nullptr;

@@ -39,6 +39,9 @@ inline size_t linear_checkpoint_rows(int B, int T, bool packed) {
   return packed ? tiles : tiles * (size_t)B;
 }
 
+// Bytes of the words through which the tiles of a call are chained (a multiple of 16).
+size_t linear_chain_bytes(int B, int T, int D, bool packed);
+
 hipError_t launch_linear_forward(const LinearArgs &p, hipStream_t stream);
 hipError_t launch_linear_backward(const LinearArgs &p, hipStream_t stream);
 // One token: h_out = a h + b x, o = h_out, N = p.B rows of p.D (p.h0: h, p.h_T: h_out).

@@ -72,13 +72,14 @@ bool pre_gates(int g) { return g == GDN2_LINEAR_PREACT || g == GDN2_LINEAR_TIED_
 
 size_t linear_forward_ws(const gdn2_linear_desc *d, bool packed) {
   if (check_linear(d) != GDN2_OK) return 0;
-  (void)packed;
-  return 0;
+  return d->B == 0 ? 0 : gdn2::linear_chain_bytes(d->B, d->T, d->D, packed);
 }
 
 size_t linear_backward_ws(const gdn2_linear_desc *d, bool packed) {
   if (check_linear(d) != GDN2_OK) return 0;
-  return gdn2::linear_checkpoint_rows(d->B, d->T, packed) * (size_t)d->D * 4;
+  return d->B == 0 ? 0
+                   : gdn2::linear_chain_bytes(d->B, d->T, d->D, packed) +
+                         gdn2::linear_checkpoint_rows(d->B, d->T, packed) * (size_t)d->D * 4;
 }
 
 gdn2_status linear_forward(const gdn2_linear_desc *d, bool packed, const int32_t *cu, const void *x, const void *a,

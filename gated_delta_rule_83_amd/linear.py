@@ -252,7 +252,7 @@ def linear_backward(x, a, b, h0, dO, dh_T=None, ck=None, want_dh0: bool = True, 
 
 def linear_backward_varlen(x, a, b, cu_seqlens, h0, dO, dh_T=None, ck=None, want_dh0: bool = True, grads=None,
                            workspace=None, stream=None, gates: str = "channel") -> dict:
-    """Gradients of linear_forward_varlen (rows outside every sequence are not written)."""
+    """Gradients of linear_forward_varlen (rows outside every sequence are zero)."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _backward(x, a, b, cu_seqlens, h0, dO, dh_T, ck, want_dh0, grads, workspace, stream, gates)
@@ -283,12 +283,7 @@ def _autograd_function():
             x, a, b, cu, h0, ck = ctx.saved_tensors
             dO = torch.zeros_like(x) if dO is None else dO.contiguous()
             dh_T = None if dh_T is None else dh_T.contiguous()
-            grads = None
-            if cu is not None:  # rows outside every sequence are not written
-                grads = {"dx": torch.zeros_like(x), "da": torch.zeros_like(a)}
-                if b is not None:
-                    grads["db"] = torch.zeros_like(b)
-            g = _backward(x, a, b, cu, h0, dO, dh_T, ck, h0 is not None, grads, None, None, ctx.gates)
+            g = _backward(x, a, b, cu, h0, dO, dh_T, ck, h0 is not None, None, None, None, ctx.gates)
             return g["dx"], g["da"], g["db"], None, g["dh0"], None
 
     return GatedLinearRecurrence

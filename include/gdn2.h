@@ -481,7 +481,7 @@ typedef struct {
  *   h0  : may be NULL (zero).   h_T : may be NULL, may be h0 itself.
  *   ck  : may be NULL; otherwise [B, ceil(T / 128), D] fp32:
  *         the states entering tokens 128, 256, ... of every sequence, which
- *         the backward takes (row 0 of each sequence is not written).
+ *         the backward takes (row 0 of each sequence is unspecified).
  *   o   : may be NULL if ck or h_T is wanted alone.
  *   workspace: gdn2_linear_forward_workspace_bytes(desc) bytes, 16-byte
  *         aligned (NULL if that is 0); scratch on entry and exit.
@@ -498,7 +498,7 @@ gdn2_status gdn2_linear_forward(const gdn2_linear_desc *desc, const void *x, con
  * outside every sequence are left as they were). h0, h_T: [B, D]; an empty
  * sequence gives h_T = h0. ck: [ceil(T / 128), D], the state entering every
  * 128th token of the packed axis where that token continues a sequence
- * (other rows are not written). */
+ * (other rows are unspecified). */
 size_t gdn2_linear_forward_varlen_workspace_bytes(const gdn2_linear_desc *desc);
 gdn2_status gdn2_linear_forward_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens, const void *x,
                                        const void *a, const void *b, const float *h0, void *o, float *h_T, float *ck,
@@ -528,7 +528,7 @@ gdn2_status gdn2_linear_backward(const gdn2_linear_desc *desc, const void *x, co
                                  void *stream);
 
 /* Gradients of gdn2_linear_forward_varlen. Gradient rows outside every
- * sequence are left as they were; an empty sequence gives dh0 = dh_T. */
+ * sequence are zero; an empty sequence gives dh0 = dh_T. */
 size_t gdn2_linear_backward_varlen_workspace_bytes(const gdn2_linear_desc *desc);
 gdn2_status gdn2_linear_backward_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens, const void *x,
                                         const void *a, const void *b, const float *h0, const float *ck,

@@ -111,6 +111,9 @@ def test_packed(lens, D, form, dtype):
     gr = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], p["dO"], p["dhT"], ck=ck, gates=form)
     torch.cuda.synchronize()
     assert (o[:lead] == 7.0).all() and (o[T - tail:] == 7.0).all()
+    for k in ("dx", "da", "db"):  # no gradient reaches a row that belongs to no sequence
+        if gr[k] is not None:
+            assert (gr[k][:lead] == 0).all() and (gr[k][T - tail:] == 0).all(), k
     check(p, [(slice(cu[n], cu[n + 1]), n) for n in range(N)], form, o, h_T, gr)
     for n in range(N):
         if cu[n] == cu[n + 1]:
