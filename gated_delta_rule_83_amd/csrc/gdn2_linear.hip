@@ -20,7 +20,7 @@ namespace gdn2 {
 
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kNT = 256, kWaves = kNT / 64;
 
 // N channels of a tensor as they lie in memory.
 template <bool BF16, int N> struct Raw;
@@ -47,10 +47,11 @@ template <> struct Raw<true, 1> {
 // Token tensors are read once, with nontemporal loads: a pass over the bytes
 // of the forward with its tiles' pattern ran at 6.16 TB/s with them and at
 // 5.23 TB/s without (bf16, 32768 x 2048).
-template <bool BF16, int N> __device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, size_t i) {
-  using T = typename Elem<BF16>::T;
+// A wave-uniform base and a 32-bit lane offset (bytes): the row's part of an
+// address costs no vector instruction.
+template <bool BF16, int N> __device__ __forceinline__ Raw<BF16, N> load_raw(const char *base, uint32_t off) {
   using V = decltype(Raw<BF16, N>::v);
-  return Raw<BF16, N>{__builtin_nontemporal_load(reinterpret_cast<const V *>(static_cast<const T *>(p) + i))};
+  return Raw<BF16, N>{__builtin_nontemporal_load(reinterpret_cast<const V *>(base + off))};
 }
 
 template <bool BF16, int N>
@@ -62,25 +63,24 @@ __device__ __forceinline__ void load_f(float (&f)[N], const void *p, size_t i) {
 }
 
 template <bool BF16, int N>
-__device__ __forceinline__ void store_f(void *p, size_t i, const float (&f)[N]) {
+__device__ __forceinline__ void store_at(char *p, const float (&f)[N]) {
   using T = typename Elem<BF16>::T;
   struct alignas(sizeof(T) * N) { T e[N]; } v;
 #pragma unroll
   for (int c = 0; c < N; ++c) Elem<BF16>::st(&v.e[c], f[c]);
-  __builtin_memcpy(__builtin_assume_aligned(static_cast<T *>(p) + i, sizeof(T) * N), &v, sizeof(v));
+  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T) * N), &v, sizeof(v));
+}
+template <bool BF16, int N> __device__ __forceinline__ void store_f(void *p, size_t i, const float (&f)[N]) {
+  store_at<BF16>(static_cast<char *>(p) + i * sizeof(typename Elem<BF16>::T), f);
 }
 
-// p = 1 / (1 + e^x) and q = 1 - p = e^x / (1 + e^x), neither by a difference:
-// both keep their relative accuracy however near the other is to 1. x above
-// 87 counts as 87, where e^x is still finite and p 1.6e-38; NaN stays. EXACT
-// (fp32 pre-activations): the reciprocal's error of one step taken out by a
-// Newton step; a bf16 pre-activation is itself off by 2^-9 of its size.
-template <bool EXACT> __device__ __forceinline__ void split_sigmoid(float x, float &p, float &q) {
-  x = x > 87.f ? 87.f : x;
-  const float e = __builtin_amdgcn_exp2f(x * 1.44269504088896341f), d = 1.f + e;
-  p = __builtin_amdgcn_rcpf(d);
-  if constexpr (EXACT) p = __builtin_fmaf(__builtin_fmaf(-d, p, 1.f), p, p);
-  q = e * p;
+// 1 / (1 + e^x). e^x may be infinite (0). EXACT (fp32 pre-activations): the
+// reciprocal's error of one step taken out by a Newton step, x above 87 as 87
+// (1.6e-38); a bf16 pre-activation is itself off by 2^-9 of its size.
+template <bool EXACT> __device__ __forceinline__ float low_sigmoid(float x) {
+  if constexpr (EXACT) x = x > 87.f ? 87.f : x;
+  const float d = 1.f + __builtin_amdgcn_exp2f(x * 1.44269504088896341f), r = __builtin_amdgcn_rcpf(d);
+  return EXACT ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r) : r;
 }
 
 template <int FORM> struct Form {
@@ -88,23 +88,24 @@ template <int FORM> struct Form {
   static constexpr bool tied = FORM == GDN2_LINEAR_TIED || FORM == GDN2_LINEAR_TIED_PREACT;
 };
 
-// The gates of a value: decay a, input gate b.
+// A value's gates from what was loaded: decay a, input gate b. 1 - a comes
+// from its own sigmoid, so that it keeps its relative accuracy as a nears 1;
+// a is then off by at most 2^-24.
 template <int FORM, bool EXACT> __device__ __forceinline__ void activate(float &a, float &b) {
-  if constexpr (Form<FORM>::pre) {
-    float q;
-    split_sigmoid<EXACT>(a, a, q);
-    if constexpr (Form<FORM>::tied)
-      b = q;
-    else
-      split_sigmoid<EXACT>(-b, b, q);
-  } else if constexpr (Form<FORM>::tied) {
+  if constexpr (FORM == GDN2_LINEAR_PREACT) {
+    a = low_sigmoid<EXACT>(a);
+    b = low_sigmoid<EXACT>(-b);
+  } else if constexpr (FORM == GDN2_LINEAR_TIED_PREACT) {
+    b = low_sigmoid<EXACT>(-a);
+    a = 1.f - b;
+  } else if constexpr (FORM == GDN2_LINEAR_TIED) {
     b = 1.f - a;
   }
 }
 
 // A sigmoid and its complement in one word: the smaller of the two, the
 // complement with its sign set. Both come back without a difference that
-// loses digits, which the gradient through the activation, p (1 - p), needs.
+// loses digits.
 __device__ __forceinline__ float pack_pair(float p, float q) { return p <= q ? p : -q; }
 __device__ __forceinline__ void unpack_pair(float v, float &p, float &q) {
   const float o = 1.f - __builtin_fabsf(v);
@@ -112,35 +113,48 @@ __device__ __forceinline__ void unpack_pair(float v, float &p, float &q) {
   q = v > 0.f ? o : -v;
 }
 
-// A token's gates as the backward keeps them (one word each) and its
-// gradients from them.
+// A token's gates as the backward keeps them, one word each. For the gradient
+// through an activation, p (1 - p), fp32 pre-activations keep both factors
+// exact to their last digits (pack_pair). With bf16 ones the word is 1 - a (or
+// b) and the other factor its difference from 1: p (1 - p) is off by at most
+// 2^-24, which a bf16 gradient shows only where p is within 2^-15 of 0 (a) or
+// of 1 (b); unpacking pairs made that kernel bound by its arithmetic
+// (B1 T65536 D2048: 512 us against 445).
 template <int FORM, bool EXACT> struct Gates {
   static __device__ __forceinline__ void pack(float &a, float &b) {
     if constexpr (Form<FORM>::pre) {
-      float p, q;
-      split_sigmoid<EXACT>(a, p, q);
-      a = pack_pair(p, q);
+      const float q = low_sigmoid<EXACT>(-a);
+      a = EXACT ? pack_pair(low_sigmoid<EXACT>(a), q) : q;
       if constexpr (!Form<FORM>::tied) {
-        split_sigmoid<EXACT>(-b, p, q);
-        b = pack_pair(p, q);
+        const float p = low_sigmoid<EXACT>(-b);
+        b = EXACT ? pack_pair(p, low_sigmoid<EXACT>(b)) : p;
       }
     }
   }
   // a, 1 - a, b, 1 - b (the complements in the pre-activation forms only)
   static __device__ __forceinline__ void unpack(float va, float vb, float &a, float &na, float &b, float &nb) {
     if constexpr (Form<FORM>::pre) {
-      unpack_pair(va, a, na);
-      if constexpr (Form<FORM>::tied)
+      if constexpr (EXACT) {
+        unpack_pair(va, a, na);
+      } else {
+        na = va;
+        a = 1.f - va;
+      }
+      if constexpr (Form<FORM>::tied) {
         b = na;
-      else
+      } else if constexpr (EXACT) {
         unpack_pair(vb, b, nb);
+      } else {
+        b = vb;
+        nb = 1.f - vb;
+      }
     } else {
       a = va;
       b = Form<FORM>::tied ? 1.f - va : vb;
     }
   }
-  static constexpr float kNone = -0.f;  // va of a token that passes the state on: a = 1
-  static __device__ __forceinline__ float none() { return Form<FORM>::pre ? kNone : 1.f; }
+  // va of a token that passes the state on (a = 1)
+  static __device__ __forceinline__ float none() { return Form<FORM>::pre ? -0.f : 1.f; }
 };
 
 struct Lin {
@@ -178,6 +192,25 @@ template <bool CUT> __device__ __forceinline__ void after(float a, float u, floa
 template <bool CUT> __device__ __forceinline__ float apply(float a, float u, float h) {
   return CUT && a == 0.f ? u : __builtin_fmaf(a, h, u);
 }
+
+// Where a tile's token tensors lie: the tile's first value, the bytes from a
+// token to the next, and this lane's offset from the tile's first value.
+template <bool BF16> struct Span {
+  size_t first;
+  uint32_t row, lane;
+  __device__ __forceinline__ Span(size_t at, int D, uint32_t lane_at) {
+    constexpr uint32_t es = sizeof(typename Elem<BF16>::T);
+    first = at * es;
+    row = (uint32_t)D * es;
+    lane = lane_at * es;
+  }
+  template <int N> __device__ __forceinline__ Raw<BF16, N> load(const void *p, int i) const {
+    return load_raw<BF16, N>(static_cast<const char *>(p) + first + (size_t)((uint64_t)row * i), lane);
+  }
+  template <int N> __device__ __forceinline__ void store(void *p, int i, const float (&f)[N]) const {
+    store_at<BF16>(static_cast<char *>(p) + first + (size_t)((uint64_t)row * i) + lane, f);
+  }
+};
 
 // Scan of the threads' maps (A, U) in token order (or, REV, from the last
 // token to the first): on return (A, U) is the map of all earlier threads of
@@ -229,8 +262,8 @@ __device__ __forceinline__ void enter(float (&in)[VEC], float (&carry)[VEC], con
   for (int c = 0; c < VEC; ++c) {
     float h = carry[c], mine = h;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = REV ? 3 - i : i;
+    for (int i = 0; i < kWaves; ++i) {
+      const int j = REV ? kWaves - 1 - i : i;
       if (j == w) mine = h;
       const float2 t = tot[j][ct * VEC + c];
       h = apply<CUT>(t.x, t.y, h);
@@ -290,23 +323,23 @@ __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 
   if (w == 0 && in != kGroup - 1 && k != ch.tiles - 1)
     __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * 64 + lane,
                        (uint64_t)word(own.x) | (uint64_t)word(own.y) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  uint64_t v[kGroup / 4];
+  uint64_t v[kGroup / kWaves];
   const uint64_t *at = ch.map + ((size_t)(k - in + w) * ch.chains + chain) * 64 + lane;
   for (int spin = 0; spin < kSpins; ++spin) {
     bool ready = true;
 #pragma unroll
-    for (int j = 0; j < kGroup / 4; ++j) {
+    for (int j = 0; j < kGroup / kWaves; ++j) {
       v[j] = 0;
-      if (4 * j + w < in)
-        v[j] = __hip_atomic_load(at + (size_t)4 * j * ch.chains * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (kWaves * j + w < in)
+        v[j] = __hip_atomic_load(at + (size_t)kWaves * j * ch.chains * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       ready = ready && v[j] != ~(uint64_t)0;
     }
     if (ready) break;
     __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
-  for (int j = 0; j < kGroup / 4; ++j)
-    maps[4 * j + w][lane] = float2{__uint_as_float((uint32_t)v[j]), __uint_as_float((uint32_t)(v[j] >> 32))};
+  for (int j = 0; j < kGroup / kWaves; ++j)
+    maps[kWaves * j + w][lane] = float2{__uint_as_float((uint32_t)v[j]), __uint_as_float((uint32_t)(v[j] >> 32))};
   __syncthreads();
   if (w != 0) return 0.f;
   float A = 1.f, U = 0.f;
@@ -333,8 +366,8 @@ __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 
 template <bool REV, bool CUT> __device__ __forceinline__ float2 tile_map(const float2 (*tot)[kLinChannels], int lane) {
   float A = 1.f, U = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = tot[REV ? 3 - i : i][lane];
+  for (int i = 0; i < kWaves; ++i) {
+    const float2 t = tot[REV ? kWaves - 1 - i : i][lane];
     after<CUT>(t.x, t.y, A, U);
   }
   return float2{A, U};
@@ -370,7 +403,7 @@ template <bool BF16, int FORM, int VEC, bool PACKED>
 __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  __shared__ float2 tot[4][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float2 tot[kWaves][kLinChannels], maps[kGroup][kLinChannels];
   __shared__ float entering[kLinChannels];
   __shared__ Edges edges[1];
   __shared__ int slot;
@@ -388,29 +421,48 @@ __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
   }
   const size_t row0 = PACKED ? 0 : (size_t)n * p.T, ck0 = PACKED ? 0 : (size_t)n * ch.tiles;
 
+  const size_t first = (row0 + t0) * D + blk * kLinChannels;
+  const uint32_t lane_at = (uint32_t)(s * G::L) * D + (cc - blk * kLinChannels);
+  const Span<BF16> sx(first, D, lane_at);
+  const Span<GB> sg(first, D, lane_at);
+  const bool ragged = t0 < lo || t0 + kLinTile > hi;
   Raw<BF16, VEC> xr[G::L];
   Raw<GB, VEC> ar[G::L], br[G::L];
+  auto load = [&](int i) {
+    xr[i] = sx.template load<VEC>(p.x, i);
+    ar[i] = sg.template load<VEC>(p.a, i);
+    if constexpr (!Form<FORM>::tied) br[i] = sg.template load<VEC>(p.b, i);
+  };
+  if (!ragged) {
 #pragma unroll
-  for (int i = 0; i < G::L; ++i) {
-    const int t = ts + i;
-    const size_t at = (row0 + (t < p.T ? t : p.T - 1)) * D + cc;
-    xr[i] = load_raw<BF16, VEC>(p.x, at);
-    ar[i] = load_raw<GB, VEC>(p.a, at);
-    if constexpr (!Form<FORM>::tied) br[i] = load_raw<GB, VEC>(p.b, at);
+    for (int i = 0; i < G::L; ++i) load(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      xr[i] = {};
+      ar[i] = br[i] = {};
+      if (ts + i < p.T) load(i);
+    }
   }
   if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
   float a[G::L][VEC], u[G::L][VEC];
 #pragma unroll
   for (int i = 0; i < G::L; ++i) {
     const int t = ts + i;
-    const bool in = t >= lo && t < hi;  // outside: the identity map
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
       float av = ar[i][c], bv = 0.f;
       if constexpr (!Form<FORM>::tied) bv = br[i][c];
       activate<FORM, !BF16>(av, bv);
-      u[i][c] = in ? bv * xr[i][c] : 0.f;
-      a[i][c] = in ? av : 1.f;
+      u[i][c] = bv * xr[i][c];
+      a[i][c] = av;
+    }
+    if (ragged && (t < lo || t >= hi)) {  // no token: the identity map
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        u[i][c] = 0.f;
+        a[i][c] = 1.f;
+      }
     }
     if constexpr (PACKED) {  // a sequence starts: its own state, and a cut
       const int q = edges[0].start[s * G::L + i];
@@ -454,8 +506,8 @@ __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
     const int t = ts + i;
 #pragma unroll
     for (int c = 0; c < VEC; ++c) h[c] = apply<PACKED>(a[i][c], u[i][c], h[c]);
-    if (own && t >= lo && t < hi) {
-      if (p.o) store_f<BF16>(p.o, (row0 + t) * D + c0, h);
+    if (own && (!ragged || (t >= lo && t < hi))) {
+      if (p.o) sx.store(p.o, i, h);
       if constexpr (PACKED) {
         const int q = edges[0].end[s * G::L + i];
         if (q >= 0 && p.h_T) store_f<false>(p.h_T, (size_t)q * D + c0, h);
@@ -471,7 +523,7 @@ template <bool BF16, int FORM, int VEC, bool PACKED>
 __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  __shared__ float2 tot[2][4][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float2 tot[2][kWaves][kLinChannels], maps[kGroup][kLinChannels];
   __shared__ float entering[kLinChannels];
   __shared__ Edges edges[1];
   __shared__ int slot;
@@ -493,16 +545,29 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   using GT = Gates<FORM, !BF16>;
   Raw<BF16, VEC> x[G::L], dr[G::L];
   float va[G::L][VEC], vb[G::L][VEC], hin[VEC];
+  const size_t first = (row0 + t0) * D + blk * kLinChannels;
+  const uint32_t lane_at = (uint32_t)(s * G::L) * D + (cc - blk * kLinChannels);
+  const Span<BF16> sx(first, D, lane_at);
+  const Span<GB> sg(first, D, lane_at);
+  const bool ragged = t0 < lo || t0 + kLinTile > hi;
   {
     Raw<GB, VEC> ar[G::L], br[G::L];
+    auto load = [&](int i) {
+      x[i] = sx.template load<VEC>(p.x, i);
+      ar[i] = sg.template load<VEC>(p.a, i);
+      if constexpr (!Form<FORM>::tied) br[i] = sg.template load<VEC>(p.b, i);
+      dr[i] = sx.template load<VEC>(p.dO, i);
+    };
+    if (!ragged) {
 #pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-      const int t = ts + i;
-      const size_t at = (row0 + (t < p.T ? t : p.T - 1)) * D + cc;
-      x[i] = load_raw<BF16, VEC>(p.x, at);
-      ar[i] = load_raw<GB, VEC>(p.a, at);
-      if constexpr (!Form<FORM>::tied) br[i] = load_raw<GB, VEC>(p.b, at);
-      dr[i] = load_raw<BF16, VEC>(p.dO, at);
+      for (int i = 0; i < G::L; ++i) load(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < G::L; ++i) {
+        x[i] = dr[i] = {};
+        ar[i] = br[i] = {};
+        if (ts + i < p.T) load(i);
+      }
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c)
@@ -510,16 +575,20 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
     if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
 #pragma unroll
     for (int i = 0; i < G::L; ++i) {
-      const bool in = ts + i >= lo && ts + i < hi;
-      if (!in) x[i].v = dr[i].v = decltype(x[i].v){};
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
         va[i][c] = ar[i][c];
         vb[i][c] = 0.f;
         if constexpr (!Form<FORM>::tied) vb[i][c] = br[i][c];
         GT::pack(va[i][c], vb[i][c]);
-        va[i][c] = in ? va[i][c] : GT::none();
-        vb[i][c] = in ? vb[i][c] : 0.f;
+      }
+      if (ragged && (ts + i < lo || ts + i >= hi)) {  // no token: the identity map
+        x[i] = dr[i] = {};
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          va[i][c] = GT::none();
+          vb[i][c] = 0.f;
+        }
       }
     }
   }
@@ -633,15 +702,14 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
         if constexpr (!Form<FORM>::tied) db[c] *= b * nb;
       }
     }
-    if (own && t < p.T) {
-      const size_t at = (row0 + t) * D + c0;
+    if (own && (!ragged || t < p.T)) {
       if (PACKED && (t < lo || t >= hi)) {  // no sequence's token: no gradient
 #pragma unroll
         for (int c = 0; c < VEC; ++c) dx[c] = da[c] = db[c] = 0.f;
       }
-      store_f<BF16>(p.dx, at, dx);
-      store_f<GB>(p.da, at, da);
-      if constexpr (!Form<FORM>::tied) store_f<GB>(p.db, at, db);
+      sx.store(p.dx, i, dx);
+      sg.store(p.da, i, da);
+      if constexpr (!Form<FORM>::tied) sg.store(p.db, i, db);
       if constexpr (PACKED) {
         const int q = edges[0].start[s * G::L + i];
         if (q >= 0 && p.dh0) store_f<false>(p.dh0, (size_t)q * D + c0, mi);

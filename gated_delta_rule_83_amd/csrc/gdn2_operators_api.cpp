@@ -49,7 +49,8 @@ gdn2_status check_linear(const gdn2_linear_desc *d) {
   if (d->dtype != GDN2_F32 && d->dtype != GDN2_BF16) return GDN2_ERR_BAD_DTYPE;
   if (d->B < 0 || d->T < 0 || d->D < 1) return GDN2_ERR_BAD_SHAPE;
   if (d->gates < GDN2_LINEAR_CHANNEL || d->gates > GDN2_LINEAR_TIED_PREACT) return GDN2_ERR_UNSUPPORTED;
-  if (d->T > INT32_MAX - 256) return GDN2_ERR_UNSUPPORTED;
+  // a tile's 128 token rows are addressed with 32-bit offsets
+  if (d->T > INT32_MAX - 256 || d->D > 1 << 22) return GDN2_ERR_UNSUPPORTED;
   // both are below 2^25 * 2^24 where the product is formed
   const size_t tiles = ceil_div((size_t)d->T, gdn2::kLinTile), blocks = ceil_div((size_t)d->D, gdn2::kLinChannels);
   const size_t per = (tiles > 0 ? tiles : 1) * blocks;

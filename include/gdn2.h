@@ -445,7 +445,7 @@ gdn2_status gdn2_chunk_backward_varlen_gates(const gdn2_desc *desc, const int32_
  *   x, o      : [B, T, D] in the input dtype
  *   a, b      : [B, T, D], by gate form (below)
  *   h0, h_T   : [B, D] fp32
- * Any B, T >= 0 and D >= 1; T <= 2^31 - 257 and B * ceil(T / 128) *
+ * Any B, T >= 0 and D >= 1; T <= 2^31 - 257, D <= 2^22 and B * ceil(T / 128) *
  * ceil(D / 64) <= 2^24 - 1 (GDN2_ERR_UNSUPPORTED beyond). Where D is a
  * multiple of 4 and every tensor 16-byte aligned, rows are moved with wide loads.
  *
