@@ -32,7 +32,8 @@ CFLAGS = ["-O3", "-std=c++20", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE,
 
 def _units():
     units = [("gdn2_api.cpp", "api", []), ("gdn2_operators_api.cpp", "operators_api", []),
-             ("gdn2_linear.hip", "linear", []), ("gdn2_norm.hip", "norm", []), ("gdn2_state_cache.hip", "state_cache", []),
+             ("gdn2_linear.hip", "linear", []), ("gdn2_norm.hip", "norm", []),
+             ("gdn2_norm.hip", "norm_backward", ["-DGDN2_NORM_BACKWARD"]), ("gdn2_state_cache.hip", "state_cache", []),
              ("gdn2_decode.hip", "decode", []),
              ("gdn2_prefill.hip", "prefill", []), ("gdn2_noalloc.hip", "noalloc", []),
              ("gdn2_backward_chunk.hip", "backward_chunk", [])]

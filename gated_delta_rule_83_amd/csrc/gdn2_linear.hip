@@ -9,8 +9,8 @@
 // (lane shuffles inside a wave, LDS across the four waves), and walks its
 // tokens again from the state that enters them. Everything between the loads
 // and the one rounding of an output is fp32.
-#include "gdn2_device.hpp"
 #include "gdn2_linear.hpp"
+#include "gdn2_vec.hpp"
 
 #include "gdn2.h"
 
@@ -22,57 +22,9 @@ namespace {
 
 constexpr int kNT = 256, kWaves = kNT / 64;
 
-// N channels of a tensor as they lie in memory.
-template <bool BF16, int N> struct Raw;
-template <> struct Raw<false, 4> {
-  floatx4 v;
-  __device__ __forceinline__ float operator[](int c) const { return v[c]; }
-};
-template <> struct Raw<true, 4> {
-  typedef uint32_t uintx2 __attribute__((ext_vector_type(2)));
-  uintx2 v;
-  __device__ __forceinline__ float operator[](int c) const {
-    return __uint_as_float(c & 1 ? v[c >> 1] & 0xffff0000u : v[c >> 1] << 16);
-  }
-};
-template <> struct Raw<false, 1> {
-  float v;
-  __device__ __forceinline__ float operator[](int) const { return v; }
-};
-template <> struct Raw<true, 1> {
-  uint16_t v;
-  __device__ __forceinline__ float operator[](int) const { return bf16_to_f32(v); }
-};
-
-// Token tensors are read once, with nontemporal loads: a pass over the bytes
-// of the forward with its tiles' pattern ran at 6.16 TB/s with them and at
-// 5.23 TB/s without (bf16, 32768 x 2048).
-// A wave-uniform base and a 32-bit lane offset (bytes): the row's part of an
-// address costs no vector instruction.
-template <bool BF16, int N> __device__ __forceinline__ Raw<BF16, N> load_raw(const char *base, uint32_t off) {
-  using V = decltype(Raw<BF16, N>::v);
-  return Raw<BF16, N>{__builtin_nontemporal_load(reinterpret_cast<const V *>(base + off))};
-}
-
-template <bool BF16, int N>
-__device__ __forceinline__ void load_f(float (&f)[N], const void *p, size_t i) {
-  using T = typename Elem<BF16>::T;
-  const Raw<BF16, N> r{*reinterpret_cast<const decltype(Raw<BF16, N>::v) *>(static_cast<const T *>(p) + i)};
-#pragma unroll
-  for (int c = 0; c < N; ++c) f[c] = r[c];
-}
-
-template <bool BF16, int N>
-__device__ __forceinline__ void store_at(char *p, const float (&f)[N]) {
-  using T = typename Elem<BF16>::T;
-  struct alignas(sizeof(T) * N) { T e[N]; } v;
-#pragma unroll
-  for (int c = 0; c < N; ++c) Elem<BF16>::st(&v.e[c], f[c]);
-  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T) * N), &v, sizeof(v));
-}
-template <bool BF16, int N> __device__ __forceinline__ void store_f(void *p, size_t i, const float (&f)[N]) {
-  store_at<BF16>(static_cast<char *>(p) + i * sizeof(typename Elem<BF16>::T), f);
-}
+// Token tensors are read with nontemporal loads (load_raw): a pass over the
+// bytes of the forward with its tiles' pattern ran at 6.16 TB/s with them and
+// at 5.23 TB/s without (bf16, 32768 x 2048).
 
 // 1 / (1 + e^x). e^x may be infinite (0). EXACT (fp32 pre-activations): the
 // reciprocal's error of one step taken out by a Newton step, x above 87 as 87
