@@ -46,39 +46,41 @@ __device__ __forceinline__ float sigmoid(float z) {
 }
 
 // ------------------------------------------------------------------ rows in registers
+// A row on LPR lanes of a wave, a workgroup of four waves taking several rows
+// at a time; or (LPR = kBlock) on the whole of a workgroup of any number of
+// waves, one row at a time.
+constexpr int kBlock = 1024;
 template <int LPR_, int NC_> struct Lanes {
-  // a workgroup of four waves with several rows at a time, or one row's own
-  static constexpr int LPR = LPR_, NC = NC_, NT = LPR > 64 ? LPR : 256, ROWS = NT / LPR;
+  static constexpr int LPR = LPR_, NC = NC_, NT = LPR == kBlock ? kBlock : 256, ROWS = NT / LPR, WAVES = NT / 64;
+  static constexpr bool BLOCK = LPR == kBlock;
+  static __device__ __forceinline__ int lanes() { return BLOCK ? (int)blockDim.x : LPR; }
+  static __device__ __forceinline__ int lane(int tid) { return BLOCK ? tid : tid % LPR; }
+  static __device__ __forceinline__ int group(int tid) { return BLOCK ? 0 : tid / LPR; }
 };
 
 // Sums of K values over a row's lanes, the same in all of them. red: K values
 // for each wave, twice (a row uses one half, the next row the other).
 template <class C, int K> __device__ __forceinline__ void row_sum(float (&x)[K], float (*red)[K], int tid) {
-  constexpr int N = C::LPR < 64 ? C::LPR : 64, W = C::LPR / 64;
+  constexpr int N = C::BLOCK ? 64 : C::LPR;
 #pragma unroll
   for (int k = 0; k < K; ++k) x[k] = lane_sum<N>(x[k]);
-  if constexpr (W > 1) {
+  if constexpr (C::BLOCK) {  // at most 16 waves' sums, one a lane of every 16
     if ((tid & 63) == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) red[tid >> 6][k] = x[k];
     }
     __syncthreads();
+    const int w = tid & 15;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      x[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) x[k] += red[w][k];
-    }
+    for (int k = 0; k < K; ++k) x[k] = lane_sum<16>(w < (int)(blockDim.x >> 6) ? red[w][k] : 0.f);
   }
 }
-
-template <class C> constexpr int kWavesOf = C::NT / 64;
 
 // A row's centred values and 1 / sqrt of their mean square.
 template <bool BF16, class C, int V>
 __device__ __forceinline__ void centre(float (&c)[C::NC][V], float &r, const Raw<BF16, V> (&x)[C::NC],
                                        const float (&one)[C::NC], const NormArgs &p, float inv,
-                                       float (*red)[kWavesOf<C>][1], int tid) {
+                                       float (*red)[C::WAVES][1], int tid) {
   float s[1] = {0.f};
 #pragma unroll
   for (int j = 0; j < C::NC; ++j) {
@@ -115,7 +117,7 @@ __device__ __forceinline__ void load_row(Raw<BF16, V> (&x)[C::NC], const void *p
   const char *base = static_cast<const char *>(p) + (size_t)row * a.D * sizeof(typename Elem<BF16>::T);
 #pragma unroll
   for (int j = 0; j < C::NC; ++j) {
-    const int col = (j * C::LPR + l) * V;
+    const int col = (j * C::lanes() + l) * V;
     x[j] = {};
     if (col < a.D) x[j] = load_raw<BF16, V>(base, col * (uint32_t)sizeof(typename Elem<BF16>::T));
   }
@@ -126,7 +128,7 @@ __device__ __forceinline__ void store_row(void *p, int64_t row, const NormArgs &
   char *base = static_cast<char *>(p) + (size_t)row * a.D * sizeof(typename Elem<BF16>::T);
 #pragma unroll
   for (int j = 0; j < C::NC; ++j) {
-    const int col = (j * C::LPR + l) * V;
+    const int col = (j * C::lanes() + l) * V;
     if (col < a.D) store_at<BF16>(base + col * (uint32_t)sizeof(typename Elem<BF16>::T), y[j]);
   }
 }
@@ -137,7 +139,7 @@ __device__ __forceinline__ void load_weights(float (&w)[C::NC][V], const void *p
   for (int j = 0; j < C::NC; ++j) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (j * C::LPR + l) * V + v;
+      const int col = (j * C::lanes() + l) * V + v;
       w[j][v] = col < a.D ? load_w(p, col, a.wbf16, none) : 0.f;
     }
   }
@@ -145,16 +147,16 @@ __device__ __forceinline__ void load_weights(float (&w)[C::NC][V], const void *p
 
 template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::NT) void norm_forward_rows(NormArgs p) {
   constexpr int NC = C::NC;
-  __shared__ float red[2][2][kWavesOf<C>][1];
-  const int tid = threadIdx.x, l = tid % C::LPR;
+  __shared__ float red[2][2][C::WAVES][1];
+  const int tid = threadIdx.x, l = C::lane(tid);
   const float inv = 1.f / (float)p.D;
   float w[NC][V], b[NC][V], one[NC];
   load_weights<V, C>(w, p.weight, p, l, 1.f);
   load_weights<V, C>(b, p.bias, p, l, 0.f);
 #pragma unroll
-  for (int j = 0; j < NC; ++j) one[j] = (j * C::LPR + l) * V < p.D ? 1.f : 0.f;
+  for (int j = 0; j < NC; ++j) one[j] = (j * C::lanes() + l) * V < p.D ? 1.f : 0.f;
   const int64_t step = (int64_t)gridDim.x * C::ROWS;
-  int64_t row = (int64_t)blockIdx.x * C::ROWS + tid / C::LPR;
+  int64_t row = (int64_t)blockIdx.x * C::ROWS + C::group(tid);
   Raw<BF16, V> x[NC], z[GATE ? NC : 1], xn[NC], zn[GATE ? NC : 1];
   if (row < p.rows) {
     load_row<BF16, V, C>(xn, p.x, row, p, l);
@@ -189,34 +191,35 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
 
 template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::NT) void norm_backward_rows(NormArgs p) {
   constexpr int NC = C::NC;
-  __shared__ float red[2][2][kWavesOf<C>][1], red2[2][kWavesOf<C>][2];
-  const int tid = threadIdx.x, l = tid % C::LPR;
+  // the next row's loads in flight; not with 16 values a lane, where 1024
+  // threads have no registers for them (270 us instead of 127 at 4096 x 16384)
+  constexpr bool AHEAD = NC * V <= 8;
+  __shared__ float red[2][2][C::WAVES][1], red2[2][C::WAVES][2];
+  const int tid = threadIdx.x, l = C::lane(tid);
   const float inv = 1.f / (float)p.D;
   float w[NC][V], b[GATE ? NC : 1][V], one[NC], dw[NC][V] = {}, db[NC][V] = {};
   load_weights<V, C>(w, p.weight, p, l, 1.f);
   if constexpr (GATE) load_weights<V, C>(b, p.bias, p, l, 0.f);
 #pragma unroll
-  for (int j = 0; j < NC; ++j) one[j] = (j * C::LPR + l) * V < p.D ? 1.f : 0.f;
+  for (int j = 0; j < NC; ++j) one[j] = (j * C::lanes() + l) * V < p.D ? 1.f : 0.f;
   const int64_t step = (int64_t)gridDim.x * C::ROWS;
-  int64_t row = (int64_t)blockIdx.x * C::ROWS + tid / C::LPR;
+  int64_t row = (int64_t)blockIdx.x * C::ROWS + C::group(tid);
   Raw<BF16, V> x[NC], y[NC], z[GATE ? NC : 1], xn[NC], yn[NC], zn[GATE ? NC : 1];
-  if (row < p.rows) {
-    load_row<BF16, V, C>(xn, p.x, row, p, l);
-    load_row<BF16, V, C>(yn, p.dy, row, p, l);
-    if constexpr (GATE) load_row<BF16, V, C>(zn, p.gate, row, p, l);
-  }
+  auto load = [&](int64_t at) {
+    load_row<BF16, V, C>(xn, p.x, at, p, l);
+    load_row<BF16, V, C>(yn, p.dy, at, p, l);
+    if constexpr (GATE) load_row<BF16, V, C>(zn, p.gate, at, p, l);
+  };
+  if (AHEAD && row < p.rows) load(row);
   for (int par = 0; row < p.rows; row += step, par ^= 1) {
+    if (!AHEAD) load(row);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       x[j] = xn[j];
       y[j] = yn[j];
       if constexpr (GATE) z[j] = zn[j];
     }
-    if (row + step < p.rows) {
-      load_row<BF16, V, C>(xn, p.x, row + step, p, l);
-      load_row<BF16, V, C>(yn, p.dy, row + step, p, l);
-      if constexpr (GATE) load_row<BF16, V, C>(zn, p.gate, row + step, p, l);
-    }
+    if (AHEAD && row + step < p.rows) load(row + step);
     float c[NC][V], d[NC][V], r, s[2] = {0.f, 0.f};
     centre<BF16, C, V>(c, r, x, one, p, inv, red[par], tid);
     if constexpr (GATE) {
@@ -263,7 +266,7 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
   // this workgroup's column sums: over its row groups, first inside a wave
   float *part = static_cast<float *>(p.workspace);
   if (!part) return;
-  __shared__ float cols[4][C::LPR > 64 ? 1 : C::LPR * V];
+  __shared__ float cols[4][C::BLOCK ? 1 : C::LPR * V];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!(k ? p.dbias : p.dweight)) continue;
@@ -271,8 +274,8 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       float(&acc)[V] = k ? db[j] : dw[j];
-      const int col = (j * C::LPR + l) * V;
-      if constexpr (C::LPR > 64) {
+      const int col = (j * C::lanes() + l) * V;
+      if constexpr (C::BLOCK) {
         if (col < p.D) store_at<false>(reinterpret_cast<char *>(to + col), acc);
       } else {
 #pragma unroll
@@ -296,91 +299,114 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
 }
 
 // ------------------------------------------------------------------ any width
-constexpr int kNT = 256;
-
-// Sum over the workgroup, the same value and rounding in every thread.
-__device__ __forceinline__ float block_sum(float x, float *red, int tid) {
-  x = lane_sum<64>(x);
-  __syncthreads();
-  if ((tid & 63) == 0) red[tid >> 6] = x;
-  __syncthreads();
-  return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
-// A row's statistics, the row read from memory for each pass.
-template <bool BF16>
-__device__ __forceinline__ void loop_stats(const typename Elem<BF16>::T *x, const NormArgs &p, float *red, int tid,
-                                           float &mean, float &r) {
-  float s = 0.f;
+// Rows too wide for registers: a workgroup a row, read from memory (or the
+// caches) again for each of its sums, V values (4 or 1) a thread at a time.
+template <bool BF16, int V>
+__device__ __forceinline__ void loop_stats(const typename Elem<BF16>::T *x, const NormArgs &p,
+                                           float (*red)[kBlock / 64][1], int tid, float &mean, float &r) {
+  using C = Lanes<kBlock, 1>;
+  float s[1] = {0.f}, f[V];
   mean = 0.f;
   if (p.layer) {
-    for (int c = tid; c < p.D; c += kNT) s += Elem<BF16>::ld(x + c);
-    mean = block_sum(s, red, tid) / (float)p.D;
-    s = 0.f;
+    for (int c = tid * V; c < p.D; c += kBlock * V) {
+      load_f<BF16>(f, x, c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[0] += f[v];
+    }
+    row_sum<C>(s, red[0], tid);
+    mean = s[0] / (float)p.D;
+    s[0] = 0.f;
   }
-  for (int c = tid; c < p.D; c += kNT) {
-    const float v = Elem<BF16>::ld(x + c) - mean;
-    s = __builtin_fmaf(v, v, s);
+  for (int c = tid * V; c < p.D; c += kBlock * V) {
+    load_f<BF16>(f, x, c);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[0] = __builtin_fmaf(f[v] - mean, f[v] - mean, s[0]);
   }
-  r = 1.f / __builtin_sqrtf(block_sum(s, red, tid) / (float)p.D + p.eps);
+  row_sum<C>(s, red[1], tid);
+  r = 1.f / __builtin_sqrtf(s[0] / (float)p.D + p.eps);
 }
 
-// Rows too wide for a workgroup's registers: one value a thread at a time.
-template <bool BF16, bool GATE> __global__ __launch_bounds__(kNT) void norm_forward_loop(NormArgs p) {
-  using E = Elem<BF16>;
-  using T = typename E::T;
-  __shared__ float red[4];
+template <bool BF16, bool GATE, int V> __global__ __launch_bounds__(kBlock) void norm_forward_loop(NormArgs p) {
+  using T = typename Elem<BF16>::T;
+  __shared__ float red[2][2][kBlock / 64][1];
   const int tid = threadIdx.x;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
     const T *x = static_cast<const T *>(p.x) + row * p.D;
-    float mean, r;
-    loop_stats<BF16>(x, p, red, tid, mean, r);
-    for (int c = tid; c < p.D; c += kNT) {
-      float y = (E::ld(x + c) - mean) * r * load_w(p.weight, c, p.wbf16, 1.f) + load_w(p.bias, c, p.wbf16, 0.f);
-      if constexpr (GATE) {
-        const float z = E::ld(static_cast<const T *>(p.gate) + row * p.D + c);
-        y *= z * sigmoid(z);
+    float mean, r, f[V], z[V];
+    loop_stats<BF16, V>(x, p, red[par], tid, mean, r);
+    for (int c = tid * V; c < p.D; c += kBlock * V) {
+      load_f<BF16>(f, x, c);
+      if constexpr (GATE) load_f<BF16>(z, p.gate, (size_t)row * p.D + c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f[v] = (f[v] - mean) * r * load_w(p.weight, c + v, p.wbf16, 1.f) + load_w(p.bias, c + v, p.wbf16, 0.f);
+        if constexpr (GATE) f[v] *= z[v] * sigmoid(z[v]);
       }
-      E::st(static_cast<T *>(p.y) + row * p.D + c, y);
+      store_f<BF16>(p.y, (size_t)row * p.D + c, f);
     }
   }
 }
 
-template <bool BF16, bool GATE> __global__ __launch_bounds__(kNT) void norm_backward_loop(NormArgs p) {
-  using E = Elem<BF16>;
-  using T = typename E::T;
-  __shared__ float red[4];
+template <bool BF16, bool GATE, int V> __global__ __launch_bounds__(kBlock) void norm_backward_loop(NormArgs p) {
+  using T = typename Elem<BF16>::T;
+  using C = Lanes<kBlock, 1>;
+  __shared__ float red[2][2][kBlock / 64][1], red2[2][kBlock / 64][2];
   const int tid = threadIdx.x;
+  // this workgroup's column sums, added to row by row: each by one thread
   float *pw = static_cast<float *>(p.workspace) + (size_t)blockIdx.x * p.D;
   float *pb = static_cast<float *>(p.workspace) + ((size_t)gridDim.x + blockIdx.x) * p.D;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T *x = static_cast<const T *>(p.x) + row * p.D, *dy = static_cast<const T *>(p.dy) + row * p.D;
-    const T *gate = static_cast<const T *>(p.gate) + row * p.D;
-    float mean, r, sd = 0.f, sx = 0.f;
-    loop_stats<BF16>(x, p, red, tid, mean, r);
-    for (int c = tid; c < p.D; c += kNT) {
-      const float xh = (E::ld(x + c) - mean) * r, w = load_w(p.weight, c, p.wbf16, 1.f);
-      float dn = E::ld(dy + c);
-      if constexpr (GATE) {
-        const float z = E::ld(gate + c), s = sigmoid(z), n = xh * w + load_w(p.bias, c, p.wbf16, 0.f);
-        if (p.dgate) E::st(static_cast<T *>(p.dgate) + row * p.D + c, dn * n * (s * (1.f + z * (1.f - s))));
-        dn *= z * s;
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
+    const size_t at = (size_t)row * p.D;
+    const T *x = static_cast<const T *>(p.x) + at;
+    const bool first = row == blockIdx.x;
+    float mean, r, s[2] = {0.f, 0.f}, f[V], d[V], z[V], acc[V];
+    loop_stats<BF16, V>(x, p, red[par], tid, mean, r);
+    for (int c = tid * V; c < p.D; c += kBlock * V) {
+      load_f<BF16>(f, x, c);
+      load_f<BF16>(d, p.dy, at + c);
+      if constexpr (GATE) load_f<BF16>(z, p.gate, at + c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f[v] = (f[v] - mean) * r;
+        const float w = load_w(p.weight, c + v, p.wbf16, 1.f);
+        if constexpr (GATE) {
+          const float sg = sigmoid(z[v]), n = f[v] * w + load_w(p.bias, c + v, p.wbf16, 0.f), dz = d[v] * n;
+          d[v] *= z[v] * sg;
+          z[v] = dz * (sg * (1.f + z[v] * (1.f - sg)));
+        }
+        s[0] += d[v] * w;
+        s[1] += d[v] * w * f[v];
       }
-      if (p.dweight) pw[c] = row == blockIdx.x ? dn * xh : pw[c] + dn * xh;
-      if (p.dbias) pb[c] = row == blockIdx.x ? dn : pb[c] + dn;
-      sd += dn * w;
-      sx += dn * w * xh;
+      if constexpr (GATE) {
+        if (p.dgate) store_f<BF16>(p.dgate, at + c, z);
+      }
+      if (p.dweight) {
+        if (!first) load_f<false>(acc, pw, c);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = first ? d[v] * f[v] : acc[v] + d[v] * f[v];
+        store_f<false>(pw, c, acc);
+      }
+      if (p.dbias) {
+        if (!first) load_f<false>(acc, pb, c);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = first ? d[v] : acc[v] + d[v];
+        store_f<false>(pb, c, acc);
+      }
     }
-    sd = p.layer ? block_sum(sd, red, tid) / (float)p.D : 0.f;
-    sx = block_sum(sx, red, tid) / (float)p.D;
-    for (int c = tid; c < p.D; c += kNT) {
-      const float xh = (E::ld(x + c) - mean) * r;
-      float dn = E::ld(dy + c);
-      if constexpr (GATE) {
-        const float z = E::ld(gate + c);
-        dn *= z * sigmoid(z);
+    row_sum<C>(s, red2[par], tid);
+    const float md = p.layer ? s[0] / (float)p.D : 0.f, mx = s[1] / (float)p.D;
+    for (int c = tid * V; c < p.D; c += kBlock * V) {
+      load_f<BF16>(f, x, c);
+      load_f<BF16>(d, p.dy, at + c);
+      if constexpr (GATE) load_f<BF16>(z, p.gate, at + c);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (GATE) d[v] *= z[v] * sigmoid(z[v]);
+        d[v] = r * (d[v] * load_w(p.weight, c + v, p.wbf16, 1.f) - (f[v] - mean) * r * mx - md);
       }
-      E::st(static_cast<T *>(p.dx) + row * p.D + c, r * (dn * load_w(p.weight, c, p.wbf16, 1.f) - xh * sx - sd));
+      store_f<BF16>(p.dx, at + c, d);
     }
   }
 }
@@ -409,14 +435,17 @@ __global__ __launch_bounds__(kReduceNT) void norm_reduce(NormArgs p, int parts) 
 }
 
 // ------------------------------------------------------------------ which kernel
-// The widest vectors every row of every tensor is aligned to (V values of at
-// most 16 bytes), and the fewest lanes that hold a row with them; wider rows
-// take more pieces a lane, then a whole workgroup. kLoop: too wide for that.
-enum Plan { k2, k4, k8, k16, k32, k64, k128, k256, k512, k1024, k1024x2, k1024x4, kLoop };
+// V: the widest vectors that every row of every tensor is aligned to (at most
+// 16 bytes). A row of up to 64 of them lies on the fewest lanes of a wave that
+// hold it, a wider one on a workgroup of as many waves as it needs, with two a
+// lane where it has more than 1024 or they are of 8 bytes; single values go
+// four to a lane. kLoop: rows too
+// wide for that.
+enum Plan { k2, k4, k8, k16, k32, k64, k16x4, k64x4, kRow, kRow2, kRow4, kLoop };
 
 struct How {
   Plan plan;
-  int vec, rows, wgs;  // values a load, rows a workgroup holds at a time, workgroups at most
+  int vec, rows, threads;  // values a load; of a workgroup: rows at a time, threads
 };
 
 uintptr_t addresses(const NormArgs &p) {
@@ -427,77 +456,95 @@ uintptr_t addresses(const NormArgs &p) {
 }
 
 How how(int D, bool bf16, uintptr_t at) {
-  static constexpr struct { int most; Plan plan; int rows, wgs; bool narrow; } of[] = {
-      {2, k2, 128, 1024, false},   {4, k4, 64, 1024, false},     {8, k8, 32, 1024, false},     {16, k16, 16, 1024, true},
-      {32, k32, 8, 1024, false},   {64, k64, 4, 1024, true},     {128, k128, 1, 1024, false},  {256, k256, 1, 1024, true},
-      {512, k512, 1, 512, false},  {1024, k1024, 1, 512, true},  {2048, k1024x2, 1, 512, false},
-      {4096, k1024x4, 1, 256, true}};
   const int wide = bf16 ? 8 : 4;
   const bool aligned = D % wide == 0 && at % 16 == 0;
   const int vec = aligned ? wide : bf16 && D % 4 == 0 && at % 8 == 0 ? 4 : 1;
   const int n = (D + vec - 1) / vec;
-  for (const auto &o : of)
-    if (n <= o.most && (aligned ? o.plan != k1024x4 : o.narrow)) return How{o.plan, vec, o.rows, o.wgs};
-  return How{kLoop, 1, 1, 1024};
-}
-
-int64_t groups(const How &h, int64_t rows) {
-  const int64_t need = (rows + h.rows - 1) / h.rows;
-  return need < h.wgs ? need : h.wgs;
-}
-
-template <bool BF16, bool GATE, bool BACK, int V, class C> void go(const NormArgs &p, unsigned grid, hipStream_t st) {
-  if constexpr (BACK)
-    hipLaunchKernelGGL((norm_backward_rows<BF16, GATE, V, C>), dim3(grid), dim3(C::NT), 0, st, p);
-  else
-    hipLaunchKernelGGL((norm_forward_rows<BF16, GATE, V, C>), dim3(grid), dim3(C::NT), 0, st, p);
-}
-
-// V narrower than 16 bytes: fewer lane counts, each for a wider range.
-template <bool BF16, bool GATE, bool BACK, int V> bool go_narrow(const NormArgs &p, Plan plan, unsigned grid, hipStream_t st) {
-  switch (plan) {
-    case k16: return go<BF16, GATE, BACK, V, Lanes<16, 1>>(p, grid, st), true;
-    case k64: return go<BF16, GATE, BACK, V, Lanes<64, 1>>(p, grid, st), true;
-    case k256: return go<BF16, GATE, BACK, V, Lanes<256, 1>>(p, grid, st), true;
-    case k1024: return go<BF16, GATE, BACK, V, Lanes<1024, 1>>(p, grid, st), true;
-    case k1024x4: return go<BF16, GATE, BACK, V, Lanes<1024, 4>>(p, grid, st), true;
-    default: return false;
+  auto row = [&](Plan plan, int nc) { return How{plan, vec, 1, ((n + nc - 1) / nc + 63) / 64 * 64}; };
+  if (vec == 1) {
+    if (n <= 16) return How{k16, vec, 16, 256};
+    if (n <= 64) return How{k16x4, vec, 16, 256};
+    if (n <= 256) return How{k64x4, vec, 4, 256};
+    if (n <= 4 * kBlock) return row(kRow4, 4);
+  } else {
+    int lanes = aligned ? 2 : 16, plan = aligned ? k2 : k16;
+    for (; lanes < n && lanes < 64; lanes *= 2) ++plan;
+    if (n <= 64) return How{(Plan)plan, vec, 256 / lanes, 256};
+    if (n <= kBlock && aligned) return row(kRow, 1);
+    if (n <= 2 * kBlock) return row(kRow2, 2);
   }
+  return How{kLoop, vec, 1, kBlock};
+}
+
+// Workgroups: 1024 threads for each compute unit (a half and the double of it
+// measured slower on most of twelve shapes, forward and backward).
+int64_t groups(const How &h, int64_t rows) {
+  const int64_t need = (rows + h.rows - 1) / h.rows, most = 256 * 1024 / h.threads;
+  return need < most ? need : most;
+}
+
+template <bool BF16, bool GATE, bool BACK, int V, class C>
+void go(const NormArgs &p, const How &h, unsigned grid, hipStream_t st) {
+  if constexpr (BACK)
+    hipLaunchKernelGGL((norm_backward_rows<BF16, GATE, V, C>), dim3(grid), dim3(h.threads), 0, st, p);
+  else
+    hipLaunchKernelGGL((norm_forward_rows<BF16, GATE, V, C>), dim3(grid), dim3(h.threads), 0, st, p);
+}
+
+template <bool BF16, bool GATE, bool BACK, int V> void go_loop(const NormArgs &p, unsigned grid, hipStream_t st) {
+  if constexpr (BACK)
+    hipLaunchKernelGGL((norm_backward_loop<BF16, GATE, V>), dim3(grid), dim3(kBlock), 0, st, p);
+  else
+    hipLaunchKernelGGL((norm_forward_loop<BF16, GATE, V>), dim3(grid), dim3(kBlock), 0, st, p);
 }
 
 template <bool BF16, bool GATE, bool BACK> void launch_g(const NormArgs &p, const How &h, unsigned grid, hipStream_t st) {
   constexpr int W = BF16 ? 8 : 4;
-  if (h.vec == W) {
+  if (h.plan != kLoop && h.vec == W) {
     switch (h.plan) {
-      case k2: return go<BF16, GATE, BACK, W, Lanes<2, 1>>(p, grid, st);
-      case k4: return go<BF16, GATE, BACK, W, Lanes<4, 1>>(p, grid, st);
-      case k8: return go<BF16, GATE, BACK, W, Lanes<8, 1>>(p, grid, st);
-      case k16: return go<BF16, GATE, BACK, W, Lanes<16, 1>>(p, grid, st);
-      case k32: return go<BF16, GATE, BACK, W, Lanes<32, 1>>(p, grid, st);
-      case k64: return go<BF16, GATE, BACK, W, Lanes<64, 1>>(p, grid, st);
-      case k128: return go<BF16, GATE, BACK, W, Lanes<128, 1>>(p, grid, st);
-      case k256: return go<BF16, GATE, BACK, W, Lanes<256, 1>>(p, grid, st);
-      case k512: return go<BF16, GATE, BACK, W, Lanes<512, 1>>(p, grid, st);
-      case k1024: return go<BF16, GATE, BACK, W, Lanes<1024, 1>>(p, grid, st);
-      default: return go<BF16, GATE, BACK, W, Lanes<1024, 2>>(p, grid, st);
+      case k2: return go<BF16, GATE, BACK, W, Lanes<2, 1>>(p, h, grid, st);
+      case k4: return go<BF16, GATE, BACK, W, Lanes<4, 1>>(p, h, grid, st);
+      case k8: return go<BF16, GATE, BACK, W, Lanes<8, 1>>(p, h, grid, st);
+      case k16: return go<BF16, GATE, BACK, W, Lanes<16, 1>>(p, h, grid, st);
+      case k32: return go<BF16, GATE, BACK, W, Lanes<32, 1>>(p, h, grid, st);
+      case k64: return go<BF16, GATE, BACK, W, Lanes<64, 1>>(p, h, grid, st);
+      case kRow: return go<BF16, GATE, BACK, W, Lanes<kBlock, 1>>(p, h, grid, st);
+      default: return go<BF16, GATE, BACK, W, Lanes<kBlock, 2>>(p, h, grid, st);
     }
   }
   if constexpr (BF16) {
-    if (h.vec == 4 && go_narrow<BF16, GATE, BACK, 4>(p, h.plan, grid, st)) return;
+    if (h.plan != kLoop && h.vec == 4) {
+      switch (h.plan) {
+        case k16: return go<BF16, GATE, BACK, 4, Lanes<16, 1>>(p, h, grid, st);
+        case k32: return go<BF16, GATE, BACK, 4, Lanes<32, 1>>(p, h, grid, st);
+        case k64: return go<BF16, GATE, BACK, 4, Lanes<64, 1>>(p, h, grid, st);
+        default: return go<BF16, GATE, BACK, 4, Lanes<kBlock, 2>>(p, h, grid, st);
+      }
+    }
   }
-  if (h.vec == 1 && go_narrow<BF16, GATE, BACK, 1>(p, h.plan, grid, st)) return;
-  if constexpr (BACK)
-    hipLaunchKernelGGL((norm_backward_loop<BF16, GATE>), dim3(grid), dim3(kNT), 0, st, p);
-  else
-    hipLaunchKernelGGL((norm_forward_loop<BF16, GATE>), dim3(grid), dim3(kNT), 0, st, p);
+  if (h.plan != kLoop) {
+    switch (h.plan) {
+      case k16: return go<BF16, GATE, BACK, 1, Lanes<16, 1>>(p, h, grid, st);
+      case k16x4: return go<BF16, GATE, BACK, 1, Lanes<16, 4>>(p, h, grid, st);
+      case k64x4: return go<BF16, GATE, BACK, 1, Lanes<64, 4>>(p, h, grid, st);
+      default: return go<BF16, GATE, BACK, 1, Lanes<kBlock, 4>>(p, h, grid, st);
+    }
+  }
+  if (h.vec > 1) return go_loop<BF16, GATE, BACK, 4>(p, grid, st);
+  go_loop<BF16, GATE, BACK, 1>(p, grid, st);
 }
 
 }  // namespace
 
 #ifdef GDN2_NORM_BACKWARD
-size_t norm_backward_workspace_bytes(int64_t rows, int D) {
-  // the most workgroups of any way to take the rows
-  return (size_t)(rows < 1024 ? rows : 1024) * D * 2 * sizeof(float);
+size_t norm_backward_workspace_bytes(int64_t rows, int D, bool bf16) {
+  // whatever the tensors' alignment
+  int64_t most = 0;
+  for (uintptr_t at : {0, 8, 2}) {
+    const int64_t g = groups(how(D, bf16, at), rows);
+    most = g > most ? g : most;
+  }
+  return (size_t)most * D * 2 * sizeof(float);
 }
 
 hipError_t launch_norm_backward(const NormArgs &q, hipStream_t st) {

@@ -22,7 +22,7 @@ struct NormArgs {
 };
 
 // Partial column sums of the weight's and the bias's gradient.
-size_t norm_backward_workspace_bytes(int64_t rows, int D);
+size_t norm_backward_workspace_bytes(int64_t rows, int D, bool bf16);
 hipError_t launch_norm_forward(const NormArgs &p, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs &p, hipStream_t stream);
 

@@ -308,7 +308,7 @@ gdn2_status gdn2_norm_forward(const gdn2_norm_desc *d, const void *x, const void
 
 size_t gdn2_norm_backward_workspace_bytes(const gdn2_norm_desc *d) {
   if (check_norm(d) != GDN2_OK) return 0;
-  return gdn2::norm_backward_workspace_bytes(d->rows, d->D);
+  return gdn2::norm_backward_workspace_bytes(d->rows, d->D, d->dtype == GDN2_BF16);
 }
 
 gdn2_status gdn2_norm_backward(const gdn2_norm_desc *d, const void *x, const void *weight, const void *bias,

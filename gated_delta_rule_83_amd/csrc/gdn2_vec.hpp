@@ -52,10 +52,10 @@ template <bool BF16, int N> __device__ __forceinline__ void load_f(float (&f)[N]
 
 template <bool BF16, int N> __device__ __forceinline__ void store_at(char *p, const float (&f)[N]) {
   using T = typename Elem<BF16>::T;
-  struct alignas(sizeof(T) * N) { T e[N]; } v;
+  struct { T e[N]; } v;
 #pragma unroll
   for (int c = 0; c < N; ++c) Elem<BF16>::st(&v.e[c], f[c]);
-  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T) * N), &v, sizeof(v));
+  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T) * N < 16 ? sizeof(T) * N : 16), &v, sizeof(v));
 }
 template <bool BF16, int N> __device__ __forceinline__ void store_f(void *p, size_t i, const float (&f)[N]) {
   store_at<BF16>(static_cast<char *>(p) + i * sizeof(typename Elem<BF16>::T), f);
