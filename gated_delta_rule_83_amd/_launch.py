@@ -1,5 +1,21 @@
-"""Where a call of the torch conveniences runs: the tensors' device and a stream of it."""
+"""Where a call of the torch conveniences runs (the tensors' device and a stream
+of it), and their argument check, kept short: for the smallest calls the host's
+time is the call's time."""
 from __future__ import annotations
+
+from . import _want
+
+
+def want(t, name, shape, dtype, device):
+    """_want, with the tensors that pass told apart first."""
+    if t is None:
+        return
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _want(t, name, tuple(shape), dtype, device)
 
 
 class launch_on:
@@ -11,28 +27,26 @@ class launch_on:
     __slots__ = ("_dev", "_stream", "_ctx")
 
     def __init__(self, device, stream):
-        self._dev, self._stream, self._ctx = device, stream, ()
+        self._dev, self._stream, self._ctx = device, stream, None
 
     def __enter__(self):
         import torch
-        if self._stream is None:
-            if torch.cuda.current_device() != self._dev.index:
-                ctx = torch.cuda.device(self._dev)
-                ctx.__enter__()
-                self._ctx = (ctx,)
-            return torch.cuda.current_stream(self._dev).cuda_stream
         s = self._stream
+        if s is None:
+            if torch.cuda.current_device() != self._dev.index:
+                self._ctx = torch.cuda.device(self._dev)
+                self._ctx.__enter__()
+            return torch._C._cuda_getCurrentRawStream(self._dev.index)
         if not hasattr(s, "cuda_stream"):
             s = (torch.cuda.ExternalStream(int(s), device=self._dev) if int(s)
                  else torch.cuda.default_stream(self._dev))
         if s.device.index != self._dev.index:
             raise ValueError(f"stream is of {s.device}, but the tensors are on {self._dev}")
-        ctx = torch.cuda.stream(s)  # makes its device current as well
-        ctx.__enter__()
-        self._ctx = (ctx,)
+        self._ctx = torch.cuda.stream(s)  # makes its device current as well
+        self._ctx.__enter__()
         return s.cuda_stream
 
     def __exit__(self, *exc):
-        for ctx in self._ctx:
-            ctx.__exit__(*exc)
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
         return False

@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, _want, load
-from ._launch import launch_on
+from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
+from ._launch import launch_on, want
 
 LINEAR_CHECKPOINT = 128
 LINEAR_GATES = {"channel": 0, "preact": 1, "tied": 2, "tied_preact": 3}
@@ -97,21 +97,21 @@ def _problem(x, a, b, cu, gates, min_dim):
     if D < 1:
         raise ValueError("x needs at least one channel")
     gdt = x.dtype if gates in ("preact", "tied_preact") else torch.float32
-    _want(x, "x", x.shape, x.dtype, dev)
+    want(x, "x", x.shape, x.dtype, dev)
     if a is None:
         raise ValueError("a is required")
-    _want(a, "a", x.shape, gdt, dev)
+    want(a, "a", x.shape, gdt, dev)
     if gates in ("tied", "tied_preact"):
         if b is not None:
             raise ValueError(f"b must be None for gates={gates!r} (it is 1 - a)")
     elif b is None:
         raise ValueError(f"b is required for gates={gates!r}")
-    _want(b, "b", x.shape, gdt, dev)
+    want(b, "b", x.shape, gdt, dev)
     tiles = -(-T // LINEAR_CHECKPOINT)
     if cu is None:
         B, rows = x.shape[0], (x.shape[0], tiles, D)
     else:
-        _want(cu, "cu_seqlens", (cu.numel(),), torch.int32, dev)
+        want(cu, "cu_seqlens", (cu.numel(),), torch.int32, dev)
         B, rows = cu.numel() - 1, (tiles, D)
         if B < 0:
             raise ValueError("cu_seqlens needs at least one offset")
@@ -123,7 +123,7 @@ def _scratch(workspace, need, dev):
     import torch
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _want(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    want(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     return workspace
 
 
@@ -131,17 +131,17 @@ def _forward(x, a, b, cu, h0, o, h_T, ck, want_state, want_checkpoints, workspac
     import torch
     desc, dev, _, B, rows = _problem(x, a, b, cu, gates, 3 if cu is None else 2)
     D, f32 = desc.D, torch.float32
-    _want(h0, "h0", (B, D), f32, dev)
+    want(h0, "h0", (B, D), f32, dev)
     with launch_on(dev, stream) as handle:
+        want(o, "o", x.shape, x.dtype, dev)
+        want(h_T, "h_T", (B, D), f32, dev)
+        want(ck, "ck", rows, f32, dev)
         if o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            o = torch.empty_like(x)
         if h_T is None and want_state:
             h_T = torch.empty((B, D), dtype=f32, device=dev)
         if ck is None and want_checkpoints:
             ck = torch.empty(rows, dtype=f32, device=dev)
-        _want(o, "o", x.shape, x.dtype, dev)
-        _want(h_T, "h_T", (B, D), f32, dev)
-        _want(ck, "ck", rows, f32, dev)
         need = (gdn2_linear_forward_workspace_bytes if cu is None else gdn2_linear_forward_varlen_workspace_bytes)(desc)
         work = _scratch(workspace, need, dev)
         ptrs = (_ptr(x), _ptr(a), _ptr(b), _ptr(h0), _ptr(o), _ptr(h_T), _ptr(ck), _ptr(work),
@@ -190,17 +190,19 @@ def linear_step(x, a, b, h, h_out=None, o=None, stream=None, gates: str = "chann
     gdt = x.dtype if gates in ("preact", "tied_preact") else torch.float32
     if a is None or (b is None) != (gates in ("tied", "tied_preact")):
         raise ValueError(f"gates={gates!r} takes a and {'no b' if gates.startswith('tied') else 'b'}")
-    _want(x, "x", shape, x.dtype, dev)
-    _want(a, "a", shape, gdt, dev)
-    _want(b, "b", shape, gdt, dev)
-    _want(h, "h", (N, D), torch.float32, dev)
+    want(x, "x", shape, x.dtype, dev)
+    want(a, "a", shape, gdt, dev)
+    want(b, "b", shape, gdt, dev)
+    want(h, "h", (N, D), torch.float32, dev)
     if h_out is None:
         h_out = h
-    _want(h_out, "h_out", (N, D), torch.float32, dev)
+    else:
+        want(h_out, "h_out", (N, D), torch.float32, dev)
     with launch_on(dev, stream) as handle:
         if o is None:
-            o = torch.empty(shape, dtype=x.dtype, device=dev)
-        _want(o, "o", shape, x.dtype, dev)
+            o = torch.empty_like(x)
+        else:
+            want(o, "o", shape, x.dtype, dev)
         st = gdn2_linear_step(gdn2_linear_desc(N, 1, D, LINEAR_GATES[gates], dtype), _ptr(x), _ptr(a), _ptr(b),
                               _ptr(h), _ptr(h_out), _ptr(o), handle)
     if st != GDN2_OK:
@@ -213,11 +215,11 @@ def _backward(x, a, b, cu, h0, dO, dh_T, ck, want_dh0, grads, workspace, stream,
     desc, dev, gdt, B, rows = _problem(x, a, b, cu, gates, 3 if cu is None else 2)
     D, f32 = desc.D, torch.float32
     for t, nm in ((h0, "h0"), (dh_T, "dh_T")):
-        _want(t, nm, (B, D), f32, dev)
+        want(t, nm, (B, D), f32, dev)
     if dO is None:
         raise ValueError("dO is required")
-    _want(dO, "dO", x.shape, x.dtype, dev)
-    _want(ck, "ck", rows, f32, dev)
+    want(dO, "dO", x.shape, x.dtype, dev)
+    want(ck, "ck", rows, f32, dev)
     g = dict(grads or {})
     shapes = {"dx": (x.shape, x.dtype), "da": (a.shape, gdt)}
     if b is not None:
@@ -228,7 +230,8 @@ def _backward(x, a, b, cu, h0, dO, dh_T, ck, want_dh0, grads, workspace, stream,
         for nm, (shape, dt) in shapes.items():
             if g.get(nm) is None:
                 g[nm] = torch.empty(shape, dtype=dt, device=dev)
-            _want(g[nm], nm, shape, dt, dev)
+            else:
+                want(g[nm], nm, shape, dt, dev)
         g = {nm: g[nm] if nm in shapes else None for nm in ("dx", "da", "db", "dh0")}
         need = (gdn2_linear_backward_workspace_bytes if cu is None
                 else gdn2_linear_backward_varlen_workspace_bytes)(desc)

@@ -8,8 +8,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, _want, load
-from ._launch import launch_on
+from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
+from ._launch import launch_on, want
 from .linear import _ref, _scratch
 
 NORM_KINDS = {"layer": 0, "rms": 1}
@@ -53,10 +53,10 @@ def _problem(x, weight, bias, gate, eps, kind):
     dev, dtype, D = x.device, _dtype_code(x), x.shape[-1]
     w = weight if weight is not None else bias
     wdt = x.dtype if w is None else w.dtype
-    _want(x, "x", x.shape, x.dtype, dev)
-    _want(weight, "weight", (D,), wdt, dev)
-    _want(bias, "bias", (D,), wdt, dev)
-    _want(gate, "gate", x.shape, x.dtype, dev)
+    want(x, "x", x.shape, x.dtype, dev)
+    want(weight, "weight", (D,), wdt, dev)
+    want(bias, "bias", (D,), wdt, dev)
+    want(gate, "gate", x.shape, x.dtype, dev)
     return gdn2_norm_desc(x.numel() // D, D, NORM_KINDS[kind], dtype, dtype if w is None else _dtype_code(w), eps), dev
 
 
@@ -67,8 +67,9 @@ def norm_forward(x, weight=None, bias=None, gate=None, eps: float = 1e-5, kind: 
     desc, dev = _problem(x, weight, bias, gate, eps, kind)
     with launch_on(dev, stream) as handle:
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _want(y, "y", x.shape, x.dtype, dev)
+            y = torch.empty_like(x)
+        else:
+            want(y, "y", x.shape, x.dtype, dev)
         st = gdn2_norm_forward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
@@ -82,7 +83,7 @@ def norm_backward(x, weight, bias, gate, dy, eps: float = 1e-5, kind: str = "lay
     wanted. `grads` may hold preallocated outputs."""
     import torch
     desc, dev = _problem(x, weight, bias, gate, eps, kind)
-    _want(dy, "dy", x.shape, x.dtype, dev)
+    want(dy, "dy", x.shape, x.dtype, dev)
     if dy is None:
         raise ValueError("dy is required")
     like = {"dx": x, "dweight": weight if want_params else None, "dbias": bias if want_params else None,
@@ -93,8 +94,9 @@ def norm_backward(x, weight, bias, gate, dy, eps: float = 1e-5, kind: str = "lay
             if t is None:
                 continue
             if g[nm] is None:
-                g[nm] = torch.empty(t.shape, dtype=t.dtype, device=dev)
-            _want(g[nm], nm, t.shape, t.dtype, dev)
+                g[nm] = torch.empty_like(t)
+            else:
+                want(g[nm], nm, t.shape, t.dtype, dev)
         work = _scratch(workspace, gdn2_norm_backward_workspace_bytes(desc), dev)
         st = gdn2_norm_backward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), _ptr(g["dx"]),
                                 _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dgate"]), _ptr(work),

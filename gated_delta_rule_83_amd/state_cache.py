@@ -7,9 +7,10 @@ A row (the last axis) shares one power-of-two scale; `fmt` is "e4m3" or "int8".
 from __future__ import annotations
 
 import ctypes
+import math
 
-from . import GDN2_OK, Gdn2Error, _ptr, _want, load
-from ._launch import launch_on
+from . import GDN2_OK, Gdn2Error, _ptr, load
+from ._launch import launch_on, want
 from .linear import _ref
 
 CACHE_FORMATS = {"e4m3": 0, "int8": 1}
@@ -54,13 +55,11 @@ def _problem(cache, scales, slots, fmt):
     if cache.dim() < 3:
         raise ValueError(f"cache must be [P, ..., rows, d_v], got {tuple(cache.shape)}")
     dev = cache.device
-    _want(cache, "cache", cache.shape, torch.uint8, dev)
-    _want(scales, "scales", cache.shape[:-1], torch.uint8, dev)
-    _want(slots, "slots", (slots.numel(),), torch.int32, dev)
-    rows = 1
-    for n in cache.shape[1:-1]:
-        rows *= n
-    return gdn2_cache_desc(slots.numel(), cache.shape[0], rows, cache.shape[-1], CACHE_FORMATS[fmt]), dev
+    want(cache, "cache", cache.shape, torch.uint8, dev)
+    want(scales, "scales", cache.shape[:-1], torch.uint8, dev)
+    want(slots, "slots", (slots.numel(),), torch.int32, dev)
+    return gdn2_cache_desc(slots.numel(), cache.shape[0], math.prod(cache.shape[1:-1]), cache.shape[-1],
+                           CACHE_FORMATS[fmt]), dev
 
 
 def state_cache_store(S, slots, cache, scales, fmt: str = "e4m3", stream=None):
@@ -69,7 +68,7 @@ def state_cache_store(S, slots, cache, scales, fmt: str = "e4m3", stream=None):
     of entries with the same slot the last is kept."""
     import torch
     desc, dev = _problem(cache, scales, slots, fmt)
-    _want(S, "S", (desc.N,) + tuple(cache.shape[1:]), torch.float32, dev)
+    want(S, "S", (desc.N,) + tuple(cache.shape[1:]), torch.float32, dev)
     with launch_on(dev, stream) as handle:
         st = gdn2_state_cache_store(desc, _ptr(S), _ptr(slots), _ptr(cache), _ptr(scales), handle)
     if st != GDN2_OK:
@@ -84,7 +83,8 @@ def state_cache_load(cache, scales, slots, S=None, fmt: str = "e4m3", stream=Non
     with launch_on(dev, stream) as handle:
         if S is None:
             S = torch.empty(shape, dtype=torch.float32, device=dev)
-        _want(S, "S", shape, torch.float32, dev)
+        else:
+            want(S, "S", shape, torch.float32, dev)
         st = gdn2_state_cache_load(desc, _ptr(cache), _ptr(scales), _ptr(slots), _ptr(S), handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
