@@ -3,11 +3,11 @@
 //
 // A token is the map h -> a h + u (u = b x); maps compose:
 //   (a2, u2) after (a1, u1) = (a2 a1, a2 u1 + u2).
-// A workgroup of 256 threads owns 64 channels and holds 128 tokens of them in
-// registers: VEC channels (one wide load) by L = 128 / slots consecutive
-// tokens a thread. It composes each thread's tokens, scans the threads' maps
-// (lane shuffles inside a wave, LDS across the four waves), and walks its
-// tokens again from the state that enters them. Everything between the loads
+// A workgroup of 256 threads owns 128 channels and holds 64 tokens of them in
+// registers: VEC channels (one wide load) by L = 64 / slots consecutive tokens
+// a thread. It composes each thread's tokens, scans the threads' maps (lane
+// shuffles inside a wave, LDS across waves), and walks its tokens again from
+// the state that enters them. Everything between the loads
 // and the one rounding of an output is fp32.
 #include "gdn2_linear.hpp"
 #include "gdn2_vec.hpp"
@@ -20,11 +20,15 @@ namespace gdn2 {
 
 namespace {
 
-constexpr int kNT = 256, kWaves = kNT / 64;
+constexpr int kNT = 256, kTeams = kNT / kLinChannels;  // threads of a workgroup, and of them per channel
+constexpr int kStepNT = 256;
 
-// Token tensors are read with nontemporal loads (load_raw): a pass over the
-// bytes of the forward with its tiles' pattern ran at 6.16 TB/s with them and
-// at 5.23 TB/s without (bf16, 32768 x 2048).
+// Token tensors are read with nontemporal loads (load_raw). A pass over the
+// bytes of the forward in tiles, bf16, 32768 x 2048: with tiles of 64 channels
+// 5.2 TB/s without them and 5.6 to 6.2 with them, with tiles of 128 channels
+// (rows of 256 bytes) 6.3 TB/s. (In the whole kernel 128 channels by 64 tokens
+// took 114 us where 64 by 128 took 124, 256 by 32 took 119, and 512 threads
+// with 128 by 128 took 154.)
 
 // 1 / (1 + e^x). e^x may be infinite (0). EXACT (fp32 pre-activations): the
 // reciprocal's error of one step taken out by a Newton step, x above 87 as 87
@@ -124,14 +128,16 @@ struct Lin {
 
 __device__ __forceinline__ int clamp_offset(int x, int T) { return x < 0 ? 0 : x > T ? T : x; }
 
-// Geometry of a thread: ct-th group of VEC channels, s-th slot of L tokens.
+// Geometry of a thread: ct-th group of VEC channels, s-th slot of L tokens;
+// WS slots a wave, in scans of PARTS parts of whole waves.
 template <int VEC> struct Geo {
-  static constexpr int CT = kLinChannels / VEC, NS = kNT / CT, L = kLinTile / NS, WS = 64 / CT;  // WS: slots a wave
+  static constexpr int CT = kLinChannels / VEC, NS = kNT / CT, L = kLinTile / NS;
+  static constexpr int PART = CT < 64 ? 64 : CT, WS = PART / CT, PARTS = kNT / PART;
 };
 
 // (A, U) := (a, u) after (A, U). CUT: a map with A = 0 takes nothing from what
 // lies before it, not even a NaN or an infinity: that is how a sequence of a
-// packed batch starts (below).
+// packed batch starts.
 template <bool CUT> __device__ __forceinline__ void after(float a, float u, float &A, float &U) {
   if (CUT && a == 0.f) {
     A = 0.f;
@@ -166,11 +172,11 @@ template <bool BF16> struct Span {
 
 // Scan of the threads' maps (A, U) in token order (or, REV, from the last
 // token to the first): on return (A, U) is the map of all earlier threads of
-// this wave, and tot[w] in LDS the whole map of wave w.
+// this part, and tot[w] in LDS the whole map of part w.
 template <int VEC, bool REV, bool CUT>
 __device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&U)[VEC], float2 (*tot)[kLinChannels], int tid) {
   using G = Geo<VEC>;
-  const int lane = tid & 63, w = tid >> 6, ct = lane % G::CT, sl = lane / G::CT;
+  const int in_part = tid % G::PART, w = tid / G::PART, ct = in_part % G::CT, sl = in_part / G::CT;
 #pragma unroll
   for (int off = 1; off < G::WS; off <<= 1) {
     const bool has = REV ? sl + off < G::WS : sl >= off;
@@ -209,13 +215,13 @@ template <int VEC, bool REV, bool CUT>
 __device__ __forceinline__ void enter(float (&in)[VEC], float (&carry)[VEC], const float (&A)[VEC],
                                       const float (&U)[VEC], const float2 (*tot)[kLinChannels], int tid) {
   using G = Geo<VEC>;
-  const int w = tid >> 6, ct = (tid & 63) % G::CT;
+  const int w = tid / G::PART, ct = tid % G::CT;
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
     float h = carry[c], mine = h;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      const int j = REV ? kWaves - 1 - i : i;
+    for (int i = 0; i < G::PARTS; ++i) {
+      const int j = REV ? G::PARTS - 1 - i : i;
       if (j == w) mine = h;
       const float2 t = tot[j][ct * VEC + c];
       h = apply<CUT>(t.x, t.y, h);
@@ -226,26 +232,26 @@ __device__ __forceinline__ void enter(float (&in)[VEC], float (&carry)[VEC], con
 }
 
 // ------------------------------------------------------------------ tiles in parallel
-// The tiles of one chain (a sequence's, or the packed axis', and 64 channels)
+// The tiles of one chain (a sequence's, or the packed axis', and 128 channels)
 // run at once, each read from memory once. A workgroup takes its chain's next
 // tile by a ticket, so that every tile it waits for was taken before it and is
 // running or done: no wait is endless. (A ticket per chain: one counter for all
-// of them hands out a tile every 15 ns, which bound the whole kernel.) It publishes its tile's map, and finds
-// the value entering the tile from
+// of them hands out a tile every 15 ns, which bound the whole kernel.) It
+// publishes its tile's map, and finds the value entering the tile from
 //   the maps of the tiles before it in its group of kGroup tiles, composed,
 //   applied to the value that left the group before (published by that
 //   group's last tile): the same sums in the same order whatever the timing.
 // Each published word validates itself (a map's two floats in 64 bits, a
 // value in 32; all bits set: not there yet; NaN published as the quiet NaN),
 // so relaxed agent-scope accesses suffice: no fence writes a cache back.
-constexpr int kGroup = 16;
+constexpr int kGroup = 8;  // 16: each tile reads twice as many maps, 1 to 4% slower
 constexpr int kTicketWords = 16;
 constexpr int kSpins = 1 << 24;  // a wait given up after this many looks yields NaN
 
 struct Chain {
   uint32_t *ticket;  // [chain], kTicketWords apart
-  uint64_t *map;    // [tile][chain][64]
-  uint32_t *value;  // [group][chain][64]
+  uint64_t *map;    // [tile][chain][kLinChannels]
+  uint32_t *value;  // [group][chain][kLinChannels]
   int chains, tiles;
 };
 
@@ -264,62 +270,64 @@ __device__ __forceinline__ void take_tile(const Chain &ch, int *slot, int tid, i
   }
 }
 
-// The value entering tile k of its chain, for this lane's channel in wave 0
+// The value entering tile k of its chain, for this thread's channel in the first kLinChannels threads
 // (start: the value entering the chain), from the tiles' published maps; own:
 // this tile's map. Publishes both. Every thread of the workgroup calls it.
 template <bool CUT>
 __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 own, float start,
                                       float2 (*maps)[kLinChannels], int tid) {
-  const int lane = tid & 63, w = tid >> 6, in = k % kGroup;
+  const int lane = tid % kLinChannels, w = tid / kLinChannels, in = k % kGroup;
   if (ch.tiles == 1) return start;
   if (w == 0 && in != kGroup - 1 && k != ch.tiles - 1)
-    __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * 64 + lane,
+    __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * kLinChannels + lane,
                        (uint64_t)word(own.x) | (uint64_t)word(own.y) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  uint64_t v[kGroup / kWaves];
-  const uint64_t *at = ch.map + ((size_t)(k - in + w) * ch.chains + chain) * 64 + lane;
+  const uint32_t *before = ch.value + ((size_t)(k / kGroup - 1) * ch.chains + chain) * kLinChannels + lane;
+  uint32_t p = ~0u;
+  auto look = [&] { p = __hip_atomic_load(before, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  if (w == 0 && k >= kGroup) look();  // mostly there before the maps are
+  uint64_t v[kGroup / kTeams];
+  const uint64_t *at = ch.map + ((size_t)(k - in + w) * ch.chains + chain) * kLinChannels + lane;
   for (int spin = 0; spin < kSpins; ++spin) {
     bool ready = true;
 #pragma unroll
-    for (int j = 0; j < kGroup / kWaves; ++j) {
+    for (int j = 0; j < kGroup / kTeams; ++j) {
       v[j] = 0;
-      if (kWaves * j + w < in)
-        v[j] = __hip_atomic_load(at + (size_t)kWaves * j * ch.chains * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (kTeams * j + w < in)
+        v[j] = __hip_atomic_load(at + (size_t)kTeams * j * ch.chains * kLinChannels, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       ready = ready && v[j] != ~(uint64_t)0;
     }
     if (ready) break;
     __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
-  for (int j = 0; j < kGroup / kWaves; ++j)
-    maps[kWaves * j + w][lane] = float2{__uint_as_float((uint32_t)v[j]), __uint_as_float((uint32_t)(v[j] >> 32))};
+  for (int j = 0; j < kGroup / kTeams; ++j)
+    maps[kTeams * j + w][lane] = float2{__uint_as_float((uint32_t)v[j]), __uint_as_float((uint32_t)(v[j] >> 32))};
   __syncthreads();
   if (w != 0) return 0.f;
   float A = 1.f, U = 0.f;
   for (int j = 0; j < in; ++j) after<CUT>(maps[j][lane].x, maps[j][lane].y, A, U);
   float h = start;
   if (k >= kGroup) {
-    uint32_t p = ~0u;
-    const uint32_t *q = ch.value + ((size_t)(k / kGroup - 1) * ch.chains + chain) * 64 + lane;
-    for (int spin = 0; spin < kSpins; ++spin) {
-      p = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (p != ~0u) break;
+    for (int spin = 0; spin < kSpins && p == ~0u; ++spin) {
       __builtin_amdgcn_s_sleep(1);
+      look();
     }
     h = __uint_as_float(p);  // all bits set is a NaN
   }
   h = apply<CUT>(A, U, h);
   if (in == kGroup - 1 && k != ch.tiles - 1)
-    __hip_atomic_store(ch.value + ((size_t)(k / kGroup) * ch.chains + chain) * 64 + lane, word(apply<CUT>(own.x, own.y, h)),
+    __hip_atomic_store(ch.value + ((size_t)(k / kGroup) * ch.chains + chain) * kLinChannels + lane, word(apply<CUT>(own.x, own.y, h)),
                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return h;
 }
 
-// A tile's map from its waves', for this lane's channel.
-template <bool REV, bool CUT> __device__ __forceinline__ float2 tile_map(const float2 (*tot)[kLinChannels], int lane) {
+// A tile's map from its parts', for one channel.
+template <int PARTS, bool REV, bool CUT>
+__device__ __forceinline__ float2 tile_map(const float2 (*tot)[kLinChannels], int channel) {
   float A = 1.f, U = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    const float2 t = tot[REV ? kWaves - 1 - i : i][lane];
+  for (int i = 0; i < PARTS; ++i) {
+    const float2 t = tot[REV ? PARTS - 1 - i : i][channel];
     after<CUT>(t.x, t.y, A, U);
   }
   return float2{A, U};
@@ -330,10 +338,17 @@ struct Edges {
   int start[kLinTile], end[kLinTile];
 };
 
+// Bit i: whether token s L + i of the tile has such an edge.
+template <int L> __device__ __forceinline__ uint32_t edge_bits(const int *at, int s) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < L; ++i) m |= at[s * L + i] >= 0 ? 1u << i : 0u;
+  return m;
+}
+
 __device__ __forceinline__ void find_edges(Edges &e, const Lin &p, int t0, int tid) {
-  if (tid < kLinTile) e.start[tid] = -1;
-  else e.end[tid - kLinTile] = -1;
-  // the first sequence that may reach into the tile, to within 256
+  if (tid < kLinTile) e.start[tid] = e.end[tid] = -1;
+  // the first sequence that may reach into the tile, to within kNT
   int lo = 0, hi = p.B;
   while (hi - lo > kNT) {
     const int mid = lo + (hi - lo) / 2;
@@ -352,14 +367,14 @@ __device__ __forceinline__ void find_edges(Edges &e, const Lin &p, int t0, int t
 }
 
 template <bool BF16, int FORM, int VEC, bool PACKED>
-__global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
+__global__ __launch_bounds__(kNT, VEC == 4 ? 4 : 1) void linear_forward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  __shared__ float2 tot[kWaves][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float2 tot[G::PARTS][kLinChannels], maps[kGroup][kLinChannels];
   __shared__ float entering[kLinChannels];
   __shared__ Edges edges[1];
   __shared__ int slot;
-  const int tid = threadIdx.x, lane = tid & 63, ct = tid % G::CT, s = tid / G::CT;
+  const int tid = threadIdx.x, lane = tid % kLinChannels, ct = tid % G::CT, s = tid / G::CT;
   int k, chain;
   take_tile(ch, &slot, tid, k, chain);
   const int n = PACKED ? 0 : chain / p.nblk, blk = chain - n * p.nblk;
@@ -396,7 +411,12 @@ __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
       if (ts + i < p.T) load(i);
     }
   }
-  if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
+  uint32_t starts = 0, ends = 0;  // of this thread's tokens
+  if constexpr (PACKED) {
+    find_edges(edges[0], p, t0, tid);
+    starts = edge_bits<G::L>(edges[0].start, s);
+    ends = edge_bits<G::L>(edges[0].end, s);
+  }
   float a[G::L][VEC], u[G::L][VEC];
 #pragma unroll
   for (int i = 0; i < G::L; ++i) {
@@ -416,35 +436,43 @@ __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
         a[i][c] = 1.f;
       }
     }
-    if constexpr (PACKED) {  // a sequence starts: its own state, and a cut
-      const int q = edges[0].start[s * G::L + i];
-      if (q >= 0) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          if (p.h0) u[i][c] = __builtin_fmaf(a[i][c], p.h0[(size_t)q * D + cc + c], u[i][c]);
-          a[i][c] = 0.f;
-        }
-      }
-    }
   }
   float A[VEC], U[VEC], h[VEC], carry[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
-    A[c] = a[0][c];
-    U[c] = u[0][c];
+    A[c] = 1.f;
+    U[c] = 0.f;
   }
+  if (!PACKED || !starts) {
 #pragma unroll
-  for (int i = 1; i < G::L; ++i) {
+    for (int i = 0; i < G::L; ++i) {
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) after<PACKED>(a[i][c], u[i][c], A[c], U[c]);
+      for (int c = 0; c < VEC; ++c) after<false>(a[i][c], u[i][c], A[c], U[c]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      if (starts >> i & 1) {  // a sequence starts: its own state, and a cut
+        const int q = edges[0].start[s * G::L + i];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          if (p.h0) u[i][c] = __builtin_fmaf(a[i][c], p.h0[(size_t)q * D + cc + c], u[i][c]);
+          A[c] = 0.f;
+          U[c] = u[i][c];
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) after<false>(a[i][c], u[i][c], A[c], U[c]);
+      }
+    }
   }
   wave_scan<VEC, false, PACKED>(A, U, tot, tid);
   __syncthreads();
   {
     const int c = blk * kLinChannels + lane;
-    const float start = !PACKED && p.h0 && c < D && tid < 64 ? p.h0[(size_t)n * D + c] : 0.f;
-    const float in = link<PACKED>(ch, k, chain, tile_map<false, PACKED>(tot, lane), start, maps, tid);
-    if (tid < 64) {
+    const float start = !PACKED && p.h0 && c < D && tid < kLinChannels ? p.h0[(size_t)n * D + c] : 0.f;
+    const float in = link<PACKED>(ch, k, chain, tile_map<G::PARTS, false, PACKED>(tot, lane), start, maps, tid);
+    if (tid < kLinChannels) {
       entering[lane] = in;
       if (p.ck && k > 0 && c < D) p.ck[(ck0 + k) * D + c] = in;
     }
@@ -453,16 +481,24 @@ __global__ __launch_bounds__(kNT) void linear_forward_chain(Lin p, Chain ch) {
 #pragma unroll
   for (int c = 0; c < VEC; ++c) carry[c] = entering[ct * VEC + c];
   enter<VEC, false, PACKED>(h, carry, A, U, tot, tid);
+  if (!PACKED || !(starts | ends)) {
 #pragma unroll
-  for (int i = 0; i < G::L; ++i) {
-    const int t = ts + i;
+    for (int i = 0; i < G::L; ++i) {
+      const int t = ts + i;
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) h[c] = apply<PACKED>(a[i][c], u[i][c], h[c]);
-    if (own && (!ragged || (t >= lo && t < hi))) {
-      if (p.o) sx.store(p.o, i, h);
-      if constexpr (PACKED) {
-        const int q = edges[0].end[s * G::L + i];
-        if (q >= 0 && p.h_T) store_f<false>(p.h_T, (size_t)q * D + c0, h);
+      for (int c = 0; c < VEC; ++c) h[c] = __builtin_fmaf(a[i][c], h[c], u[i][c]);
+      if (own && p.o && (!ragged || (t >= lo && t < hi))) sx.store(p.o, i, h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      const int t = ts + i;
+      const bool cut = starts >> i & 1;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = cut ? u[i][c] : __builtin_fmaf(a[i][c], h[c], u[i][c]);
+      if (own && t >= lo && t < hi) {
+        if (p.o) sx.store(p.o, i, h);
+        if ((ends >> i & 1) && p.h_T) store_f<false>(p.h_T, (size_t)edges[0].end[s * G::L + i] * D + c0, h);
       }
     }
   }
@@ -475,11 +511,12 @@ template <bool BF16, int FORM, int VEC, bool PACKED>
 __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  __shared__ float2 tot[2][kWaves][kLinChannels], maps[kGroup][kLinChannels];
+  __shared__ float2 tot[2][G::PARTS][kLinChannels], maps[kGroup][kLinChannels];
   __shared__ float entering[kLinChannels];
   __shared__ Edges edges[1];
+  __shared__ float last[PACKED ? kLinTile : 1][kLinChannels];
   __shared__ int slot;
-  const int tid = threadIdx.x, lane = tid & 63, ct = tid % G::CT, s = tid / G::CT;
+  const int tid = threadIdx.x, lane = tid % kLinChannels, ct = tid % G::CT, s = tid / G::CT;
   int k, chain;
   take_tile(ch, &slot, tid, k, chain);
   const int n = PACKED ? 0 : chain / p.nblk, blk = chain - n * p.nblk;
@@ -524,7 +561,6 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c)
       hin[c] = tile > 0 ? p.ck[(ck0 + tile) * D + cc + c] : !PACKED && p.h0 ? p.h0[(size_t)n * D + cc + c] : 0.f;
-    if constexpr (PACKED) find_edges(edges[0], p, t0, tid);
 #pragma unroll
     for (int i = 0; i < G::L; ++i) {
 #pragma unroll
@@ -544,16 +580,18 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
       }
     }
   }
-  // the outputs' gradients; a packed sequence's last token adds its state's,
-  // read before anything is published (dh0 may be dh_T)
-  float dE[PACKED ? G::L : 1][VEC];
+  // a packed sequence's last token takes its state's gradient too: read before
+  // anything is published (dh0 may be dh_T) and kept where only this thread looks
+  uint32_t starts = 0, ends = 0;
   if constexpr (PACKED) {
-#pragma unroll
-    for (int i = 0; i < G::L; ++i) {
-      const int q = edges[0].end[s * G::L + i];
+    find_edges(edges[0], p, t0, tid);
+    starts = edge_bits<G::L>(edges[0].start, s);
+    ends = edge_bits<G::L>(edges[0].end, s);
+    for (uint32_t m = ends; m; m &= m - 1) {
+      const int at = s * G::L + __builtin_ctz(m);
 #pragma unroll
       for (int c = 0; c < VEC; ++c)
-        dE[i][c] = dr[i][c] + (q >= 0 && p.dh_T ? p.dh_T[(size_t)q * D + cc + c] : 0.f);
+        last[at][ct * VEC + c] = p.dh_T ? p.dh_T[(size_t)edges[0].end[at] * D + cc + c] : 0.f;
     }
   }
   // between the passes over the tokens: what is unpacked for one pass is not
@@ -565,39 +603,47 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
       if constexpr (!Form<FORM>::tied) pin_regs(vb[i]);
       if constexpr (sizeof(x[i]) % 4 == 0) {
         pin_regs(x[i].v);
-        if constexpr (!PACKED) pin_regs(dr[i].v);
+        pin_regs(dr[i].v);
       }
     }
   };
-  auto dO = [&](int i, int c) { return PACKED ? dE[PACKED ? i : 0][c] : dr[i][c]; };
   float A[VEC], U[VEC], Am[VEC], Um[VEC], h[VEC], mi[VEC], m[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
     A[c] = Am[c] = 1.f;
     U[c] = Um[c] = 0.f;
   }
+  if (!PACKED || !(starts | ends)) {
 #pragma unroll
-  for (int i = 0; i < G::L; ++i) {
-    const int j = G::L - 1 - i;
-    const int q = PACKED ? edges[0].start[s * G::L + i] : -1;
-    const bool cut = PACKED && edges[0].end[s * G::L + j] >= 0;
+    for (int i = 0; i < G::L; ++i) {
+      const int j = G::L - 1 - i;
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      float a, na, b, nb, am, x0, x1, x2;
-      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
-      GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
-      const float u = b * x[i][c];
-      if constexpr (PACKED) {
-        if (q >= 0)
-          after<true>(0.f, p.h0 ? __builtin_fmaf(a, p.h0[(size_t)q * D + cc + c], u) : u, A[c], U[c]);
-        else
-          after<true>(a, u, A[c], U[c]);
-        after<true>(cut ? 0.f : am, am * dO(j, c), Am[c], Um[c]);
-      } else {
-        U[c] = __builtin_fmaf(a, U[c], u);
+      for (int c = 0; c < VEC; ++c) {
+        float a, b, am, x0, x1, x2;
+        GT::unpack(va[i][c], vb[i][c], a, x0, b, x1);
+        GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
+        U[c] = __builtin_fmaf(a, U[c], b * x[i][c]);
         A[c] *= a;
-        Um[c] = am * (dO(j, c) + Um[c]);
-        Am[c] = A[c];
+        Um[c] = am * (dr[j][c] + Um[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) Am[c] = A[c];
+  } else {
+#pragma unroll
+    for (int i = 0; i < G::L; ++i) {
+      const int j = G::L - 1 - i;
+      const bool first = starts >> i & 1, cut = ends >> j & 1;
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        float a, b, am, x0, x1, x2;
+        GT::unpack(va[i][c], vb[i][c], a, x0, b, x1);
+        GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
+        const float from = first ? (p.h0 ? p.h0[(size_t)edges[0].start[s * G::L + i] * D + cc + c] : 0.f) : U[c];
+        U[c] = __builtin_fmaf(a, from, b * x[i][c]);
+        A[c] = first ? 0.f : A[c] * a;
+        Um[c] = am * (dr[j][c] + (cut ? last[s * G::L + j][ct * VEC + c] : Um[c]));
+        Am[c] = cut ? 0.f : Am[c] * am;
       }
     }
   }
@@ -607,20 +653,17 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   __syncthreads();
   {
     const int c = blk * kLinChannels + lane;
-    const float start = !PACKED && p.dh_T && c < D && tid < 64 ? p.dh_T[(size_t)n * D + c] : 0.f;
-    const float in = link<PACKED>(ch, k, chain, tile_map<true, PACKED>(tot[1], lane), start, maps, tid);
-    if (tid < 64) entering[lane] = in;
+    const float start = !PACKED && p.dh_T && c < D && tid < kLinChannels ? p.dh_T[(size_t)n * D + c] : 0.f;
+    const float in = link<PACKED>(ch, k, chain, tile_map<G::PARTS, true, PACKED>(tot[1], lane), start, maps, tid);
+    if (tid < kLinChannels) entering[lane] = in;
   }
   enter<VEC, false, PACKED>(h, hin, A, U, tot[0], tid);
   float hp[G::L][VEC];
 #pragma unroll
   for (int i = 0; i < G::L; ++i) {
-    if constexpr (PACKED) {
-      const int q = edges[0].start[s * G::L + i];
-      if (q >= 0) {
+    if (PACKED && (starts >> i & 1)) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) h[c] = p.h0 ? p.h0[(size_t)q * D + cc + c] : 0.f;
-      }
+      for (int c = 0; c < VEC; ++c) h[c] = p.h0 ? p.h0[(size_t)edges[0].start[s * G::L + i] * D + cc + c] : 0.f;
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
@@ -639,12 +682,15 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   for (int i = G::L - 1; i >= 0; --i) {
     const int t = ts + i;
     float dx[VEC], da[VEC], db[VEC];
-    const bool cut = PACKED && edges[0].end[s * G::L + i] >= 0;
+    if (PACKED && (ends >> i & 1)) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) mi[c] = last[s * G::L + i][ct * VEC + c];
+    }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
       float a, na, b, nb;
       GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
-      const float g = dO(i, c) + (cut ? 0.f : mi[c]), xv = x[i][c];
+      const float g = dr[i][c] + mi[c], xv = x[i][c];
       mi[c] = a * g;
       dx[c] = b * g;
       db[c] = xv * g;
@@ -655,17 +701,15 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
       }
     }
     if (own && (!ragged || t < p.T)) {
-      if (PACKED && (t < lo || t >= hi)) {  // no sequence's token: no gradient
+      if (PACKED && ragged && (t < lo || t >= hi)) {  // no sequence's token: no gradient
 #pragma unroll
         for (int c = 0; c < VEC; ++c) dx[c] = da[c] = db[c] = 0.f;
       }
       sx.store(p.dx, i, dx);
       sg.store(p.da, i, da);
       if constexpr (!Form<FORM>::tied) sg.store(p.db, i, db);
-      if constexpr (PACKED) {
-        const int q = edges[0].start[s * G::L + i];
-        if (q >= 0 && p.dh0) store_f<false>(p.dh0, (size_t)q * D + c0, mi);
-      }
+      if (PACKED && (starts >> i & 1) && p.dh0)
+        store_f<false>(p.dh0, (size_t)edges[0].start[s * G::L + i] * D + c0, mi);
     }
   }
   if (!PACKED && p.dh0 && tile == 0 && own && s == 0) store_f<false>(p.dh0, (size_t)n * D + c0, m);
@@ -686,9 +730,9 @@ __global__ __launch_bounds__(kNT) void chain_prepare(uint4 *words, size_t count,
 
 // One token: a thread per VEC channels of a row.
 template <bool BF16, int FORM, int VEC>
-__global__ __launch_bounds__(kNT) void linear_step(Lin p, size_t total) {
+__global__ __launch_bounds__(kStepNT) void linear_step(Lin p, size_t total) {
   constexpr bool GB = BF16 && Form<FORM>::pre;
-  for (size_t i = ((size_t)blockIdx.x * kNT + threadIdx.x) * VEC; i < total; i += (size_t)gridDim.x * kNT * VEC) {
+  for (size_t i = ((size_t)blockIdx.x * kStepNT + threadIdx.x) * VEC; i < total; i += (size_t)gridDim.x * kStepNT * VEC) {
     float a[VEC], b[VEC], x[VEC], h[VEC];
     load_f<false>(h, p.h0, i);
     load_f<GB>(a, p.a, i);
@@ -709,7 +753,8 @@ enum Op { kForward, kBackward, kStep };
 // Bytes of a chained launch's words: the tickets, the maps, the values.
 size_t chain_bytes(int chains, int tiles) {
   if (tiles <= 1) return 0;
-  return (size_t)chains * (kTicketWords * 4 + (size_t)tiles * 64 * 8 + (size_t)((tiles + kGroup - 1) / kGroup) * 64 * 4);
+  return (size_t)chains * (kTicketWords * 4 + (size_t)tiles * kLinChannels * 8 +
+                           (size_t)((tiles + kGroup - 1) / kGroup) * kLinChannels * 4);
 }
 
 template <bool BF16, int FORM, int VEC>
@@ -717,9 +762,9 @@ hipError_t launch_v(const LinearArgs &q, Op op, hipStream_t st) {
   Lin p{q.x, q.a, q.b, q.h0, q.o, q.h_T, q.ck, q.dO, q.dh_T, q.dx, q.da, q.db, q.dh0, q.cu, q.B, q.T, q.D, 0};
   p.nblk = (q.D + kLinChannels - 1) / kLinChannels;
   if (op == kStep) {
-    const size_t total = (size_t)q.B * q.D, per = (size_t)kNT * VEC;
+    const size_t total = (size_t)q.B * q.D, per = (size_t)kStepNT * VEC;
     const size_t wgs = (total + per - 1) / per;
-    hipLaunchKernelGGL((linear_step<BF16, FORM, VEC>), dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(kNT), 0, st, p,
+    hipLaunchKernelGGL((linear_step<BF16, FORM, VEC>), dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(kStepNT), 0, st, p,
                        total);
     return hipGetLastError();
   }
@@ -730,7 +775,7 @@ hipError_t launch_v(const LinearArgs &q, Op op, hipStream_t st) {
   if (bytes) {
     ch.ticket = static_cast<uint32_t *>(q.workspace);
     ch.map = reinterpret_cast<uint64_t *>(ch.ticket + (size_t)ch.chains * kTicketWords);
-    ch.value = reinterpret_cast<uint32_t *>(ch.map + (size_t)ch.tiles * ch.chains * 64);
+    ch.value = reinterpret_cast<uint32_t *>(ch.map + (size_t)ch.tiles * ch.chains * kLinChannels);
   }
   const float *from = op == kForward ? q.h0 : q.dh_T;
   float *to = !q.cu && ch.tiles ? nullptr : op == kForward ? q.h_T : q.dh0;

@@ -9,9 +9,9 @@
 namespace gdn2 {
 
 // Tokens a workgroup holds at once, and the spacing of the saved states.
-constexpr int kLinTile = 128;
+constexpr int kLinTile = 64;
 // Channels a workgroup owns.
-constexpr int kLinChannels = 64;
+constexpr int kLinChannels = 128;
 
 struct LinearArgs {
   int B, T, D;

@@ -16,7 +16,7 @@ import ctypes
 from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
 from ._launch import launch_on, want
 
-LINEAR_CHECKPOINT = 128
+LINEAR_CHECKPOINT = 64
 LINEAR_GATES = {"channel": 0, "preact": 1, "tied": 2, "tied_preact": 3}
 
 
@@ -162,7 +162,7 @@ def linear_forward(x, a, b=None, h0=None, o=None, h_T=None, ck=None, want_state:
     """h_t = a_t h_{t-1} + b_t x_t over whole sequences. x [B,T,D] (bf16 or
     fp32); a, b [B,T,D] by gate form; h0 [B,D] fp32 or None. Returns
     (o [B,T,D], h_T [B,D] fp32), and with want_checkpoints the states saved for
-    the backward, ck [B,ceil(T/128),D] fp32."""
+    the backward, ck [B,ceil(T/64),D] fp32."""
     return _forward(x, a, b, None, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
 
 
@@ -170,7 +170,7 @@ def linear_forward_varlen(x, a, b, cu_seqlens, h0=None, o=None, h_T=None, ck=Non
                           want_checkpoints: bool = False, workspace=None, stream=None, gates: str = "channel"):
     """linear_forward over N packed sequences: x, a, b [T,D]; cu_seqlens int32
     [N+1] on the device (sequence n = rows cu[n]..cu[n+1]-1; rows outside every
-    sequence are not written); h0, h_T [N,D]; ck [ceil(T/128),D]."""
+    sequence are not written); h0, h_T [N,D]; ck [ceil(T/64),D]."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     return _forward(x, a, b, cu_seqlens, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
@@ -270,7 +270,7 @@ def _autograd_function():
     from torch.autograd.function import once_differentiable
 
     class GatedLinearRecurrence(torch.autograd.Function):
-        """o, h_T of the recurrence; saves the inputs and one state per 128 tokens."""
+        """o, h_T of the recurrence; saves the inputs and one state per 64 tokens."""
 
         @staticmethod
         def forward(ctx, x, a, b, cu_seqlens, h0, gates):

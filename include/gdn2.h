@@ -445,8 +445,8 @@ gdn2_status gdn2_chunk_backward_varlen_gates(const gdn2_desc *desc, const int32_
  *   x, o      : [B, T, D] in the input dtype
  *   a, b      : [B, T, D], by gate form (below)
  *   h0, h_T   : [B, D] fp32
- * Any B, T >= 0 and D >= 1; T <= 2^31 - 257, D <= 2^22 and B * ceil(T / 128) *
- * ceil(D / 64) <= 2^24 - 1 (GDN2_ERR_UNSUPPORTED beyond). Where D is a
+ * Any B, T >= 0 and D >= 1; T <= 2^31 - 257, D <= 2^22 and B * ceil(T / 64) *
+ * ceil(D / 128) <= 2^24 - 1 (GDN2_ERR_UNSUPPORTED beyond). Where D is a
  * multiple of 4 and every tensor 16-byte aligned, rows are moved with wide loads.
  *
  * Gate forms:
@@ -475,12 +475,12 @@ typedef struct {
 } gdn2_linear_desc;
 
 /* Tokens between two saved states (ck below). */
-#define GDN2_LINEAR_CHECKPOINT 128
+#define GDN2_LINEAR_CHECKPOINT 64
 
 /* Whole sequences.
  *   h0  : may be NULL (zero).   h_T : may be NULL, may be h0 itself.
- *   ck  : may be NULL; otherwise [B, ceil(T / 128), D] fp32:
- *         the states entering tokens 128, 256, ... of every sequence, which
+ *   ck  : may be NULL; otherwise [B, ceil(T / 64), D] fp32:
+ *         the states entering tokens 64, 128, ... of every sequence, which
  *         the backward takes (row 0 of each sequence is unspecified).
  *   o   : may be NULL if ck or h_T is wanted alone.
  *   workspace: gdn2_linear_forward_workspace_bytes(desc) bytes, 16-byte
@@ -496,8 +496,8 @@ gdn2_status gdn2_linear_forward(const gdn2_linear_desc *desc, const void *x, con
  * tokens cu_seqlens[n] .. cu_seqlens[n+1]-1 (B + 1 non-decreasing int32 device
  * offsets, clamped to [0, T]; they need not cover all T tokens: rows of o
  * outside every sequence are left as they were). h0, h_T: [B, D]; an empty
- * sequence gives h_T = h0. ck: [ceil(T / 128), D], the state entering every
- * 128th token of the packed axis where that token continues a sequence
+ * sequence gives h_T = h0. ck: [ceil(T / 64), D], the state entering every
+ * 64th token of the packed axis where that token continues a sequence
  * (other rows are unspecified). */
 size_t gdn2_linear_forward_varlen_workspace_bytes(const gdn2_linear_desc *desc);
 gdn2_status gdn2_linear_forward_varlen(const gdn2_linear_desc *desc, const int32_t *cu_seqlens, const void *x,

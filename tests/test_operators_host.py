@@ -92,7 +92,7 @@ def test_linear_backward_pointers_and_workspace():
     assert bwd(lin(), put(f, _10=f[6] + 64)) == g.GDN2_ERR_ALIAS
     assert bwd(lin(), put(f, _7=f[8])) == g.GDN2_ERR_ALIAS
     need = g.gdn2_linear_backward_workspace_bytes(lin())
-    assert need >= 2 * 3 * 64 * 4  # the states every 128 tokens
+    assert need >= 2 * 3 * 64 * 4  # the states every 64 tokens
     assert bwd(lin(), f, need - 1) == g.GDN2_ERR_WORKSPACE and bwd(lin(), f, 0) == g.GDN2_ERR_WORKSPACE
     assert g.gdn2_linear_backward(lin(), *f, f[0], need, 0) == g.GDN2_ERR_ALIAS
     assert g.gdn2_linear_backward(lin(), *f, FAKE - EACH + 4, need, 0) == g.GDN2_ERR_BAD_SHAPE
