@@ -18,6 +18,14 @@ def want(t, name, shape, dtype, device):
     _want(t, name, tuple(shape), dtype, device)
 
 
+def no_second_order(name):
+    """The gradients come from a kernel that autograd cannot see into; grad mode
+    is on in a backward only for create_graph=True."""
+    import torch
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no second derivatives (create_graph=True)")
+
+
 class launch_on:
     """with launch_on(device, stream) as handle: the tensors' device is current,
     new tensors belong to the launch's stream, and handle is that stream's

@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 
 from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
-from ._launch import launch_on, want
+from ._launch import launch_on, no_second_order, want
 
 LINEAR_CHECKPOINT = 64
 LINEAR_GATES = {"channel": 0, "preact": 1, "tied": 2, "tied_preact": 3}
@@ -127,34 +127,39 @@ def _scratch(workspace, need, dev):
     return workspace
 
 
+def _launch_forward(desc, x, a, b, cu, h0, o, h_T, ck, workspace, handle):
+    """A checked problem, on its device and stream."""
+    need = (gdn2_linear_forward_workspace_bytes if cu is None else gdn2_linear_forward_varlen_workspace_bytes)(desc)
+    work = _scratch(workspace, need, x.device)
+    ptrs = (_ptr(x), _ptr(a), _ptr(b), _ptr(h0), _ptr(o), _ptr(h_T), _ptr(ck), _ptr(work),
+            work.numel() if work is not None else 0, handle)
+    if not (x.numel() or (desc.B and h_T is not None)):
+        st = GDN2_OK
+    elif cu is None:
+        st = gdn2_linear_forward(desc, *ptrs)
+    else:
+        st = gdn2_linear_forward_varlen(desc, _ptr(cu), *ptrs)
+    if st != GDN2_OK:
+        raise Gdn2Error(st)
+
+
 def _forward(x, a, b, cu, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates):
     import torch
     desc, dev, _, B, rows = _problem(x, a, b, cu, gates, 3 if cu is None else 2)
     D, f32 = desc.D, torch.float32
     want(h0, "h0", (B, D), f32, dev)
+    want(o, "o", x.shape, x.dtype, dev)
+    want(h_T, "h_T", (B, D), f32, dev)
+    want(ck, "ck", rows, f32, dev)
     with launch_on(dev, stream) as handle:
-        want(o, "o", x.shape, x.dtype, dev)
-        want(h_T, "h_T", (B, D), f32, dev)
-        want(ck, "ck", rows, f32, dev)
         if o is None:
             o = torch.empty_like(x)
         if h_T is None and want_state:
             h_T = torch.empty((B, D), dtype=f32, device=dev)
         if ck is None and want_checkpoints:
             ck = torch.empty(rows, dtype=f32, device=dev)
-        need = (gdn2_linear_forward_workspace_bytes if cu is None else gdn2_linear_forward_varlen_workspace_bytes)(desc)
-        work = _scratch(workspace, need, dev)
-        ptrs = (_ptr(x), _ptr(a), _ptr(b), _ptr(h0), _ptr(o), _ptr(h_T), _ptr(ck), _ptr(work),
-                work.numel() if work is not None else 0, handle)
-        if not B or not (x.numel() or h_T is not None):
-            st = GDN2_OK
-        elif cu is None:
-            st = gdn2_linear_forward(desc, *ptrs)
-        else:
-            st = gdn2_linear_forward_varlen(desc, _ptr(cu), *ptrs)
-    if st != GDN2_OK:
-        raise Gdn2Error(st)
-    return (o, h_T, ck) if want_checkpoints else (o, h_T)
+        _launch_forward(desc, x, a, b, cu, h0, o, h_T, ck, workspace, handle)
+    return desc, o, h_T, ck
 
 
 def linear_forward(x, a, b=None, h0=None, o=None, h_T=None, ck=None, want_state: bool = True,
@@ -163,7 +168,8 @@ def linear_forward(x, a, b=None, h0=None, o=None, h_T=None, ck=None, want_state:
     fp32); a, b [B,T,D] by gate form; h0 [B,D] fp32 or None. Returns
     (o [B,T,D], h_T [B,D] fp32), and with want_checkpoints the states saved for
     the backward, ck [B,ceil(T/64),D] fp32."""
-    return _forward(x, a, b, None, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
+    out = _forward(x, a, b, None, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
+    return out[1:] if want_checkpoints else out[1:3]
 
 
 def linear_forward_varlen(x, a, b, cu_seqlens, h0=None, o=None, h_T=None, ck=None, want_state: bool = True,
@@ -173,7 +179,8 @@ def linear_forward_varlen(x, a, b, cu_seqlens, h0=None, o=None, h_T=None, ck=Non
     sequence are not written); h0, h_T [N,D]; ck [ceil(T/64),D]."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    return _forward(x, a, b, cu_seqlens, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
+    out = _forward(x, a, b, cu_seqlens, h0, o, h_T, ck, want_state, want_checkpoints, workspace, stream, gates)
+    return out[1:] if want_checkpoints else out[1:3]
 
 
 def linear_step(x, a, b, h, h_out=None, o=None, stream=None, gates: str = "channel"):
@@ -210,6 +217,17 @@ def linear_step(x, a, b, h, h_out=None, o=None, stream=None, gates: str = "chann
     return o
 
 
+def _launch_backward(desc, x, a, b, cu, h0, ck, dO, dh_T, g, workspace, handle):
+    """A checked problem, on its device and stream; g: dx, da, db, dh0."""
+    need = (gdn2_linear_backward_workspace_bytes if cu is None else gdn2_linear_backward_varlen_workspace_bytes)(desc)
+    work = _scratch(workspace, need, x.device)
+    ptrs = (_ptr(x), _ptr(a), _ptr(b), _ptr(h0), _ptr(ck), _ptr(dO), _ptr(dh_T), *map(_ptr, g), _ptr(work),
+            work.numel() if work is not None else 0, handle)
+    st = gdn2_linear_backward(desc, *ptrs) if cu is None else gdn2_linear_backward_varlen(desc, _ptr(cu), *ptrs)
+    if st != GDN2_OK:
+        raise Gdn2Error(st)
+
+
 def _backward(x, a, b, cu, h0, dO, dh_T, ck, want_dh0, grads, workspace, stream, gates) -> dict:
     import torch
     desc, dev, gdt, B, rows = _problem(x, a, b, cu, gates, 3 if cu is None else 2)
@@ -220,27 +238,18 @@ def _backward(x, a, b, cu, h0, dO, dh_T, ck, want_dh0, grads, workspace, stream,
         raise ValueError("dO is required")
     want(dO, "dO", x.shape, x.dtype, dev)
     want(ck, "ck", rows, f32, dev)
-    g = dict(grads or {})
-    shapes = {"dx": (x.shape, x.dtype), "da": (a.shape, gdt)}
-    if b is not None:
-        shapes["db"] = (b.shape, gdt)
-    if want_dh0:
-        shapes["dh0"] = ((B, D), f32)
+    grads = grads or {}
+    shapes = {"dx": (x.shape, x.dtype), "da": (a.shape, gdt), "db": None if b is None else (b.shape, gdt),
+              "dh0": ((B, D), f32) if want_dh0 else None}
+    g = {}
     with launch_on(dev, stream) as handle:
-        for nm, (shape, dt) in shapes.items():
-            if g.get(nm) is None:
-                g[nm] = torch.empty(shape, dtype=dt, device=dev)
-            else:
-                want(g[nm], nm, shape, dt, dev)
-        g = {nm: g[nm] if nm in shapes else None for nm in ("dx", "da", "db", "dh0")}
-        need = (gdn2_linear_backward_workspace_bytes if cu is None
-                else gdn2_linear_backward_varlen_workspace_bytes)(desc)
-        work = _scratch(workspace, need, dev)
-        ptrs = (_ptr(x), _ptr(a), _ptr(b), _ptr(h0), _ptr(ck), _ptr(dO), _ptr(dh_T), _ptr(g["dx"]), _ptr(g["da"]),
-                _ptr(g["db"]), _ptr(g["dh0"]), _ptr(work), work.numel() if work is not None else 0, handle)
-        st = gdn2_linear_backward(desc, *ptrs) if cu is None else gdn2_linear_backward_varlen(desc, _ptr(cu), *ptrs)
-    if st != GDN2_OK:
-        raise Gdn2Error(st)
+        for nm, like in shapes.items():
+            g[nm] = t = None if like is None else grads.get(nm)
+            if like is not None and t is None:
+                g[nm] = torch.empty(like[0], dtype=like[1], device=dev)
+            elif t is not None:
+                want(t, nm, *like, dev)
+        _launch_backward(desc, x, a, b, cu, h0, ck, dO, dh_T, g.values(), workspace, handle)
     return g
 
 
@@ -267,27 +276,30 @@ _FN = None
 
 def _autograd_function():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class GatedLinearRecurrence(torch.autograd.Function):
-        """o, h_T of the recurrence; saves the inputs and one state per 64 tokens."""
+        """o, h_T of the recurrence; saves the inputs and one state per 64
+        tokens. The forward has checked the tensors and autograd gives
+        gradients of its outputs' shapes and types: the backward launches."""
 
         @staticmethod
         def forward(ctx, x, a, b, cu_seqlens, h0, gates):
-            o, h_T, ck = _forward(x, a, b, cu_seqlens, h0, None, None, None, True, True, None, None, gates)
+            ctx.desc, o, h_T, ck = _forward(x, a, b, cu_seqlens, h0, None, None, None, True, True, None, None, gates)
             ctx.save_for_backward(x, a, b, cu_seqlens, h0, ck)
-            ctx.gates = gates
             ctx.set_materialize_grads(False)
             return o, h_T
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, dO, dh_T):
+            no_second_order("gated_linear_recurrence")
             x, a, b, cu, h0, ck = ctx.saved_tensors
-            dO = torch.zeros_like(x) if dO is None else dO.contiguous()
-            dh_T = None if dh_T is None else dh_T.contiguous()
-            g = _backward(x, a, b, cu, h0, dO, dh_T, ck, h0 is not None, None, None, None, ctx.gates)
-            return g["dx"], g["da"], g["db"], None, g["dh0"], None
+            with launch_on(x.device, None) as handle:
+                dO = torch.zeros_like(x) if dO is None else dO.contiguous()
+                dh_T = None if dh_T is None else dh_T.contiguous()
+                empty = torch.empty_like
+                g = (empty(x), empty(a), None if b is None else empty(b), None if h0 is None else empty(h0))
+                _launch_backward(ctx.desc, x, a, b, cu, h0, ck, dO, dh_T, g, None, handle)
+            return g[0], g[1], g[2], None, g[3], None
 
     return GatedLinearRecurrence
 

@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 
 from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
-from ._launch import launch_on, want
+from ._launch import launch_on, no_second_order, want
 from .linear import _ref, _scratch
 
 NORM_KINDS = {"layer": 0, "rms": 1}
@@ -60,20 +60,23 @@ def _problem(x, weight, bias, gate, eps, kind):
     return gdn2_norm_desc(x.numel() // D, D, NORM_KINDS[kind], dtype, dtype if w is None else _dtype_code(w), eps), dev
 
 
-def norm_forward(x, weight=None, bias=None, gate=None, eps: float = 1e-5, kind: str = "layer", y=None, stream=None):
-    """x, gate [..., D] (bf16 or fp32); weight, bias [D] of one type (bf16 or
-    fp32) or None. Returns y like x."""
+def _forward(x, weight, bias, gate, eps, kind, y, stream):
     import torch
     desc, dev = _problem(x, weight, bias, gate, eps, kind)
+    want(y, "y", x.shape, x.dtype, dev)
     with launch_on(dev, stream) as handle:
         if y is None:
             y = torch.empty_like(x)
-        else:
-            want(y, "y", x.shape, x.dtype, dev)
         st = gdn2_norm_forward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
-    return y
+    return desc, y
+
+
+def norm_forward(x, weight=None, bias=None, gate=None, eps: float = 1e-5, kind: str = "layer", y=None, stream=None):
+    """x, gate [..., D] (bf16 or fp32); weight, bias [D] of one type (bf16 or
+    fp32) or None. Returns y like x."""
+    return _forward(x, weight, bias, gate, eps, kind, y, stream)[1]
 
 
 def norm_backward(x, weight, bias, gate, dy, eps: float = 1e-5, kind: str = "layer", want_params: bool = True,
@@ -97,13 +100,17 @@ def norm_backward(x, weight, bias, gate, dy, eps: float = 1e-5, kind: str = "lay
                 g[nm] = torch.empty_like(t)
             else:
                 want(g[nm], nm, t.shape, t.dtype, dev)
-        work = _scratch(workspace, gdn2_norm_backward_workspace_bytes(desc), dev)
-        st = gdn2_norm_backward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), _ptr(g["dx"]),
-                                _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(g["dgate"]), _ptr(work),
-                                work.numel() if work is not None else 0, handle)
+        _launch_backward(desc, x, weight, bias, gate, dy, g.values(), workspace, handle)
+    return g
+
+
+def _launch_backward(desc, x, weight, bias, gate, dy, g, workspace, handle):
+    """A checked problem, on its device and stream; g: dx, dweight, dbias, dgate."""
+    work = _scratch(workspace, gdn2_norm_backward_workspace_bytes(desc), x.device)
+    st = gdn2_norm_backward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), *map(_ptr, g), _ptr(work),
+                            work.numel() if work is not None else 0, handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
-    return g
 
 
 # ------------------------------------------------------------------ autograd
@@ -112,26 +119,29 @@ _FN = None
 
 def _autograd_function():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class GatedNorm(torch.autograd.Function):
-        """norm_forward; saves its inputs (the statistics are computed again)."""
+        """norm_forward; saves its inputs (the statistics are computed again).
+        The forward has checked the tensors and autograd gives a gradient of y's
+        shape and type: the backward launches."""
 
         @staticmethod
         def forward(ctx, x, weight, bias, gate, eps, kind):
-            y = norm_forward(x, weight, bias, gate, eps=eps, kind=kind)
+            ctx.desc, y = _forward(x, weight, bias, gate, eps, kind, None, None)
             ctx.save_for_backward(x, weight, bias, gate)
-            ctx.eps, ctx.kind = eps, kind
             return y
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, dy):
+            no_second_order("norm")
             x, weight, bias, gate = ctx.saved_tensors
-            g = norm_backward(x, weight, bias, gate, dy.contiguous(), eps=ctx.eps, kind=ctx.kind,
-                              want_params=ctx.needs_input_grad[1] or ctx.needs_input_grad[2],
-                              want_dgate=ctx.needs_input_grad[3])
-            return g["dx"], g["dweight"], g["dbias"], g["dgate"], None, None
+            need = ctx.needs_input_grad
+            with launch_on(x.device, None) as handle:
+                empty = torch.empty_like
+                g = (empty(x), empty(weight) if need[1] else None, empty(bias) if need[2] else None,
+                     empty(gate) if need[3] else None)
+                _launch_backward(ctx.desc, x, weight, bias, gate, dy.contiguous(), g, None, handle)
+            return g + (None, None)
 
     return GatedNorm
 

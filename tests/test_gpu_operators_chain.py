@@ -115,3 +115,25 @@ def test_training():
         size = np.sqrt(((R.f64(grads[k]) * v) ** 2).sum())
         print(f"[chain gradient {k}] {got:.8g} {num:.8g}", flush=True)
         assert abs(got - num) <= 1.6e-2 * size + 1e-3
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(2, 5, 8, device=DEV, requires_grad=True)
+    a = torch.rand(2, 5, 8, device=DEV)
+    for y in (g.gated_linear_recurrence(x, a, a)[0], g.norm(x)):
+        with pytest.raises(RuntimeError, match="second derivatives"):
+            torch.autograd.grad(y.sum(), x, create_graph=True)
+
+
+def test_parts_of_a_graph_that_are_not_used():
+    """Only the last state in the loss, frozen gates and weights, a gradient that is a view of one number."""
+    x = torch.randn(2, 70, 8, device=DEV, requires_grad=True)
+    a, b = torch.rand(2, 70, 8, device=DEV), torch.rand(2, 70, 8, device=DEV)
+    h_T = g.gated_linear_recurrence(x, a, b)[1]
+    dx = torch.autograd.grad(h_T.sum(), x)[0]
+    ref = g.linear_backward(x.detach(), a, b, None, torch.zeros_like(a), torch.ones(2, 8, device=DEV))["dx"]
+    assert torch.equal(dx, ref)
+    w = torch.ones(8, device=DEV)
+    z = torch.randn(2, 70, 8, device=DEV)
+    dx = torch.autograd.grad(g.norm(x, w, w, z).sum(), x)[0]
+    assert torch.equal(dx, g.norm_backward(x.detach(), w, w, z, torch.ones_like(z))["dx"])
