@@ -48,7 +48,7 @@ const char *gdn2_status_string(gdn2_status s) {
     case GDN2_OK: return "ok";
     case GDN2_ERR_NULL_POINTER: return "a required pointer is NULL";
     case GDN2_ERR_BAD_SHAPE: return "invalid shape, or a tensor pointer not 16-byte aligned";
-    case GDN2_ERR_UNSUPPORTED: return "unsupported head dimension or chunk length, or token rows too wide for a chunk's buffer range";
+    case GDN2_ERR_UNSUPPORTED: return "not built: a head dimension, chunk length, gate form, kind or format, or sizes beyond a launch's or a buffer's range";
     case GDN2_ERR_BAD_DTYPE: return "unknown dtype";
     case GDN2_ERR_WORKSPACE: return "workspace too small";
     case GDN2_ERR_HIP: return "HIP runtime error at launch";

@@ -197,8 +197,7 @@ gdn2_status check_cache(const gdn2_cache_desc *d) {
   if (d->N < 0 || d->P < 0 || d->rows < 1 || d->d_v < 1) return GDN2_ERR_BAD_SHAPE;
   if (d->format != GDN2_CACHE_E4M3 && d->format != GDN2_CACHE_INT8) return GDN2_ERR_UNSUPPORTED;
   if (d->d_v != 16 && d->d_v != 32 && d->d_v != 64 && d->d_v != 128) return GDN2_ERR_UNSUPPORTED;
-  // a workgroup takes at least 64 rows
-  if (d->rows > INT32_MAX - 4096 || ceil_div((size_t)d->rows, 64) * (size_t)d->N > kMaxGroups)
+  if (d->rows > INT32_MAX - 4096 || gdn2::state_cache_groups(d->rows, d->d_v) * (size_t)d->N > kMaxGroups)
     return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;
 }

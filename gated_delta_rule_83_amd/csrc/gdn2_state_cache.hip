@@ -147,7 +147,8 @@ __global__ __launch_bounds__(kNT) void load_kernel(StateCacheArgs p, int per_ent
 }
 
 template <int FMT, int DV> hipError_t launch(const StateCacheArgs &p, bool store, hipStream_t st) {
-  const int per = (p.rows + Rows<DV>::BLOCK - 1) / Rows<DV>::BLOCK;
+  const int per = (int)state_cache_groups(p.rows, DV);
+  static_assert(Rows<DV>::BLOCK == 2 * 256 / (DV / 8), "state_cache_groups");
   const dim3 grid((unsigned)((size_t)p.N * per));
   if (store)
     hipLaunchKernelGGL((store_kernel<FMT, DV>), grid, dim3(kNT), 0, st, p, per);

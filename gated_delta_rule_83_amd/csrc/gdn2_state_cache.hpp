@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace gdn2 {
@@ -14,6 +15,12 @@ struct StateCacheArgs {
   const int32_t *slots;
   uint8_t *cache, *scales;
 };
+
+// Workgroups of one state: 256 threads take 8 values each of two rows.
+inline size_t state_cache_groups(int rows, int d_v) {
+  const size_t per = 2 * 256 / (d_v / 8);
+  return ((size_t)rows + per - 1) / per;
+}
 
 hipError_t launch_state_cache_store(const StateCacheArgs &p, hipStream_t stream);
 hipError_t launch_state_cache_load(const StateCacheArgs &p, hipStream_t stream);

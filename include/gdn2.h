@@ -59,7 +59,7 @@ typedef enum {
                                 a tensor pointer not 16-byte aligned (4-byte for the
                                 tensors of one fp32 per token and value head:
                                 beta, alpha and their gradients) */
-  GDN2_ERR_UNSUPPORTED = 3,  /* valid but not built: d_k, d_v not in {16,32,64,128}, chunk not in {16,32,64},
+  GDN2_ERR_UNSUPPORTED = 3,  /* valid but not built (the delta rule; each other operator lists its own): d_k, d_v not in {16,32,64,128}, chunk not in {16,32,64},
                                 or (prefill and backward) max(H_qk, H_v) * max(d_k, d_v) * 4 * 64 > 2^31 - 1
                                 (one chunk of the widest token rows must fit a buffer range:
                                 H <= 65535 at d = 128) */
@@ -544,7 +544,8 @@ gdn2_status gdn2_linear_backward_varlen(const gdn2_linear_desc *desc, const int3
  *
  *   x, gate, y : [rows, D] in desc->dtype; gate may be NULL (no factor)
  *   weight, bias : [D] in desc->wdtype; either may be NULL (ones, zeros)
- * Any rows >= 0, D >= 1; eps >= 0. Sums are fp32. Tensors need only be aligned
+ * Any rows >= 0, D >= 1; eps >= 0. Sums are fp32 (magnitudes above about 1e18
+ * overflow the mean square). Tensors need only be aligned
  * to their elements; where D is a multiple of 8 and they are 16-byte aligned,
  * rows are moved with wide loads. */
 typedef enum { GDN2_NORM_LAYER = 0, GDN2_NORM_RMS = 1 } gdn2_norm_kind;

@@ -121,7 +121,20 @@ def test_packed(lens, D, form, dtype):
     again = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], p["dO"], p["dhT"], gates=form)
     for k in ("dx", "da", "db"):
         if gr[k] is not None:
-            assert torch.equal(gr[k][lead:T - tail], again[k][lead:T - tail]), k
+            assert torch.equal(gr[k], again[k]), k
+    # no initial states, no gradients of the last ones
+    z = dict(p, h0=torch.zeros_like(p["h0"]), dhT=torch.zeros_like(p["dhT"]))
+    o, h_T = g.linear_forward_varlen(p["x"], p["a"], p["b"], cud, gates=form)
+    gr = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, None, p["dO"], gates=form)
+    torch.cuda.synchronize()
+    check(z, [(slice(cu[n], cu[n + 1]), n) for n in range(N)], form, o, h_T, gr)
+    # states in place
+    h, d = p["h0"].clone(), p["dhT"].clone()
+    T2 = g.linear_forward_varlen(p["x"], p["a"], p["b"], cud, h, h_T=h, gates=form)[1]
+    g2 = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], p["dO"], d, grads={"dh0": d}, gates=form)
+    torch.cuda.synchronize()
+    assert T2 is h and g2["dh0"] is d
+    check(p, [(slice(cu[n], cu[n + 1]), n) for n in range(N)], form, keep, h, dict(again, dh0=d))
 
 
 @pytest.mark.parametrize("D", [5, 64])
@@ -157,21 +170,23 @@ def test_decays_of_zero_and_one(value):
         assert np.abs(R.f64(o[n]) - ro).max() <= 2 * 700 * R.U32 * np.abs(ro).max()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("form", ["preact", "tied_preact"])
-def test_far_preactivations(form):
+def test_far_preactivations(form, dtype):
     """Pre-activations of +-100 and +-inf: decays of 1 and 0 to within 2e-38, and finite gradients."""
     T, D = 6, 4
     pre = torch.tensor([-100.0, -float("inf"), -90.0, 100.0, float("inf"), 90.0], device=DEV)
     a = pre[None, :, None].expand(1, T, D).contiguous()
     b = None if form == "tied_preact" else (-pre)[None, :, None].expand(1, T, D).contiguous()
-    x = torch.ones(1, T, D, device=DEV)
+    x = torch.ones(1, T, D, device=DEV).to(R.TORCH[dtype])
+    a, b = a.to(x.dtype), None if b is None else b.to(x.dtype)
     h0 = torch.full((1, D), 3.0, device=DEV)
     o, _ = g.linear_forward(x, a, b, h0, gates=form)
     gr = g.linear_backward(x, a, b, h0, torch.ones_like(x), gates=form)
     torch.cuda.synchronize()
     # tied: the first three keep 3, then h = x = 1; with an input gate of sigmoid(-pre): 3 + 1 + 1 + 1, then 0
     want = [3, 3, 3, 1, 1, 1] if form == "tied_preact" else [4, 5, 6, 0, 0, 0]
-    assert (o[0, :, 0].cpu() - torch.tensor(want, dtype=torch.float32)).abs().max() <= 1e-30
+    assert (o[0, :, 0].float().cpu() - torch.tensor(want, dtype=torch.float32)).abs().max() <= 1e-30
     assert all(torch.isfinite(v).all() for v in gr.values() if v is not None)
 
 
@@ -313,3 +328,14 @@ def test_offsets_past_32_bits():
     close("o", o[1, T - last:, cols], ro, np.abs(ro).max(), torch.bfloat16)
     close("h_T", h_T[1, cols], rT, np.abs(ro).max())
     assert (o[0] == 0).all()
+    del o
+    # the gradients of the last tokens: what lies before them weighs less than 0.2^250
+    dO = torch.zeros_like(x)
+    dO[1, T - 50:, cols] = x[1, T - 50:, cols]
+    gr = g.linear_backward(x, a, None, None, dO, gates="tied_preact")
+    torch.cuda.synchronize()
+    sl = (1, slice(T - last, None), cols)
+    dx, da, _, _, ad = R.linear_grads(R.f64(x[sl]), R.f64(a[sl]), None, np.zeros(5), R.f64(dO[sl]), np.zeros(5), "tied_preact")
+    close("dx", gr["dx"][sl], dx, np.abs(ad).max(), torch.bfloat16)
+    close("da", gr["da"][sl], da, np.abs(ad).max() * 2 * np.abs(R.f64(x[sl])).max(), torch.bfloat16, 2.0)
+    assert (gr["dx"][0] == 0).all()

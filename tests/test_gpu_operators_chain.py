@@ -137,3 +137,31 @@ def test_parts_of_a_graph_that_are_not_used():
     z = torch.randn(2, 70, 8, device=DEV)
     dx = torch.autograd.grad(g.norm(x, w, w, z).sum(), x)[0]
     assert torch.equal(dx, g.norm_backward(x.detach(), w, w, z, torch.ones_like(z))["dx"])
+
+
+def test_a_captured_training_step():
+    """Forward and backward through autograd in one graph, replayed on new inputs, eager work between."""
+    mk = lambda *s: torch.randn(*s, device=DEV)
+    x, a, h0, w, dy = mk(1, 400, 64), torch.rand(1, 400, 64, device=DEV), mk(1, 64), mk(64), mk(1, 400, 64)
+
+    def step():
+        leaf = [t.detach().requires_grad_() for t in (x, a, h0, w)]
+        o, h_T = g.gated_linear_recurrence(leaf[0], leaf[1], None, leaf[2], gates="tied")
+        y = g.norm(o, leaf[3], kind="rms")
+        return [y.detach(), h_T.detach(), *torch.autograd.grad((y, h_T), leaf, (dy, h0))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        x.copy_(mk(1, 400, 64))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for u, v in zip(got, step()):
+            assert torch.equal(u, v), i

@@ -45,7 +45,7 @@ def put(p, **at):
 BAD_LINEAR = [(None, g.GDN2_ERR_NULL_POINTER), (lin(dtype=2), g.GDN2_ERR_BAD_DTYPE), (lin(B=-1), g.GDN2_ERR_BAD_SHAPE),
               (lin(T=-1), g.GDN2_ERR_BAD_SHAPE), (lin(D=0), g.GDN2_ERR_BAD_SHAPE), (lin(gates=4), g.GDN2_ERR_UNSUPPORTED),
               (lin(gates=-1), g.GDN2_ERR_UNSUPPORTED), (lin(T=2 ** 31 - 1), g.GDN2_ERR_UNSUPPORTED),
-              (lin(B=2 ** 31 - 1, D=2 ** 31 - 1), g.GDN2_ERR_UNSUPPORTED), (lin(B=2 ** 24), g.GDN2_ERR_UNSUPPORTED)]
+              (lin(B=2 ** 31 - 1, D=2 ** 31 - 1), g.GDN2_ERR_UNSUPPORTED), (lin(D=2 ** 22 + 1), g.GDN2_ERR_UNSUPPORTED), (lin(B=2 ** 24), g.GDN2_ERR_UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("desc,status", BAD_LINEAR)
@@ -157,7 +157,8 @@ def cch(N=3, P=9, rows=2048, d_v=128, fmt=0):
     (None, g.GDN2_ERR_NULL_POINTER), (cch(N=-1), g.GDN2_ERR_BAD_SHAPE), (cch(P=-1), g.GDN2_ERR_BAD_SHAPE),
     (cch(rows=0), g.GDN2_ERR_BAD_SHAPE), (cch(d_v=0), g.GDN2_ERR_BAD_SHAPE), (cch(d_v=48), g.GDN2_ERR_UNSUPPORTED),
     (cch(fmt=2), g.GDN2_ERR_UNSUPPORTED), (cch(rows=2 ** 31 - 1), g.GDN2_ERR_UNSUPPORTED),
-    (cch(N=2 ** 24), g.GDN2_ERR_UNSUPPORTED)])
+    (cch(N=2 ** 24), g.GDN2_ERR_UNSUPPORTED),
+    (cch(N=2 ** 18, rows=32 * 64), g.GDN2_ERR_UNSUPPORTED)])
 def test_cache_descriptions(desc, status):
     assert g.gdn2_state_cache_store(desc, *fakes(4)) == status
     assert g.gdn2_state_cache_load(desc, *fakes(4)) == status
