@@ -438,8 +438,9 @@ __global__ __launch_bounds__(kReduceNT) void norm_reduce(NormArgs p, int parts) 
 // V: the widest vectors that every row of every tensor is aligned to (at most
 // 16 bytes). A row of up to 64 of them lies on the fewest lanes of a wave that
 // hold it, a wider one on a workgroup of as many waves as it needs, with two a
-// lane where it has more than 1024 or they are of 8 bytes; single values go
-// four to a lane. kLoop: rows too
+// lane where it has more than 256 (8192 x 8192 bf16, forward: 55 us, with one
+// 68; at 256 the two are even) or they are of 8 bytes; single values go four to
+// a lane. kLoop: rows too
 // wide for that.
 enum Plan { k2, k4, k8, k16, k32, k64, k16x4, k64x4, kRow, kRow2, kRow4, kLoop };
 
@@ -455,7 +456,9 @@ uintptr_t addresses(const NormArgs &p) {
   return at;
 }
 
-How how(int D, bool bf16, uintptr_t at) {
+// pairs: whether a lane's registers hold two vectors well (not with a gate in
+// the backward, 137 against 304 us at 16384 x 4096).
+How how(int D, bool bf16, uintptr_t at, bool pairs) {
   const int wide = bf16 ? 8 : 4;
   const bool aligned = D % wide == 0 && at % 16 == 0;
   const int vec = aligned ? wide : bf16 && D % 4 == 0 && at % 8 == 0 ? 4 : 1;
@@ -470,7 +473,7 @@ How how(int D, bool bf16, uintptr_t at) {
     int lanes = aligned ? 2 : 16, plan = aligned ? k2 : k16;
     for (; lanes < n && lanes < 64; lanes *= 2) ++plan;
     if (n <= 64) return How{(Plan)plan, vec, 256 / lanes, 256};
-    if (n <= kBlock && aligned) return row(kRow, 1);
+    if (aligned && n <= (pairs ? 256 : kBlock)) return row(kRow, 1);
     if (n <= 2 * kBlock) return row(kRow2, 2);
   }
   return How{kLoop, vec, 1, kBlock};
@@ -538,11 +541,13 @@ template <bool BF16, bool GATE, bool BACK> void launch_g(const NormArgs &p, cons
 
 #ifdef GDN2_NORM_BACKWARD
 size_t norm_backward_workspace_bytes(int64_t rows, int D, bool bf16) {
-  // whatever the tensors' alignment
+  // whatever the tensors' alignment, with a gate or without
   int64_t most = 0;
   for (uintptr_t at : {0, 8, 2}) {
-    const int64_t g = groups(how(D, bf16, at), rows);
-    most = g > most ? g : most;
+    for (bool pairs : {false, true}) {
+      const int64_t g = groups(how(D, bf16, at, pairs), rows);
+      most = g > most ? g : most;
+    }
   }
   return (size_t)most * D * 2 * sizeof(float);
 }
@@ -550,7 +555,7 @@ size_t norm_backward_workspace_bytes(int64_t rows, int D, bool bf16) {
 hipError_t launch_norm_backward(const NormArgs &q, hipStream_t st) {
   NormArgs p = q;
   if (!p.dweight && !p.dbias) p.workspace = nullptr;
-  const How h = how(p.D, p.bf16, addresses(p));
+  const How h = how(p.D, p.bf16, addresses(p), !p.gate);
   const int64_t parts = groups(h, p.rows);
   if (parts > 0) {
     const unsigned g = (unsigned)parts;
@@ -565,7 +570,7 @@ hipError_t launch_norm_backward(const NormArgs &q, hipStream_t st) {
 }
 #else
 hipError_t launch_norm_forward(const NormArgs &p, hipStream_t st) {
-  const How h = how(p.D, p.bf16, addresses(p));
+  const How h = how(p.D, p.bf16, addresses(p), true);
   const unsigned g = (unsigned)groups(h, p.rows);
   if (p.bf16)
     p.gate ? launch_g<true, true, false>(p, h, g, st) : launch_g<true, false, false>(p, h, g, st);
