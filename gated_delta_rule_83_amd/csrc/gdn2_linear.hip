@@ -172,39 +172,34 @@ template <bool BF16> struct Span {
 
 // Scan of the threads' maps (A, U) in token order (or, REV, from the last
 // token to the first): on return (A, U) is the map of all earlier threads of
-// this part, and tot[w] in LDS the whole map of part w.
+// this part, and tot[w] in LDS the whole map of part w. A part is one slot
+// (VEC = 1), or a wave of two, whose halves swap their maps in registers.
 template <int VEC, bool REV, bool CUT>
 __device__ __forceinline__ void wave_scan(float (&A)[VEC], float (&U)[VEC], float2 (*tot)[kLinChannels], int tid) {
   using G = Geo<VEC>;
-  const int in_part = tid % G::PART, w = tid / G::PART, ct = in_part % G::CT, sl = in_part / G::CT;
-#pragma unroll
-  for (int off = 1; off < G::WS; off <<= 1) {
-    const bool has = REV ? sl + off < G::WS : sl >= off;
+  static_assert(G::WS == 1 || (G::WS == 2 && G::CT == 32), "slots of a part");
+  const int w = tid / G::PART, ct = tid % G::CT;
+  if constexpr (G::WS == 1) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      const float pa = REV ? __shfl_down(A[c], off * G::CT, 64) : __shfl_up(A[c], off * G::CT, 64);
-      const float pu = REV ? __shfl_down(U[c], off * G::CT, 64) : __shfl_up(U[c], off * G::CT, 64);
-      if (has) {
-        U[c] = apply<CUT>(A[c], U[c], pu);
-        A[c] = CUT && A[c] == 0.f ? 0.f : A[c] * pa;
-      }
-    }
-  }
-  if (sl == (REV ? 0 : G::WS - 1)) {
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) tot[w][ct * VEC + c] = float2{A[c], U[c]};
-  }
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) {
-    if constexpr (G::WS == 1) {
+      tot[w][ct * VEC + c] = float2{A[c], U[c]};
       A[c] = 1.f;
       U[c] = 0.f;
-    } else {
-      const float pa = REV ? __shfl_down(A[c], G::CT, 64) : __shfl_up(A[c], G::CT, 64);
-      const float pu = REV ? __shfl_down(U[c], G::CT, 64) : __shfl_up(U[c], G::CT, 64);
-      const bool first = REV ? sl == G::WS - 1 : sl == 0;
-      A[c] = first ? 1.f : pa;
-      U[c] = first ? 0.f : pu;
+    }
+  } else {
+    const bool later = ((tid & 32) != 0) != REV;  // this half comes after the other one
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      // [0]: the lower half's value in both halves, [1]: the upper half's
+      const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(A[c]), __float_as_uint(A[c]), false, false);
+      const auto u = __builtin_amdgcn_permlane32_swap(__float_as_uint(U[c]), __float_as_uint(U[c]), false, false);
+      const float a0 = __uint_as_float(a[REV ? 1 : 0]), u0 = __uint_as_float(u[REV ? 1 : 0]);
+      A[c] = a0;
+      U[c] = u0;
+      after<CUT>(__uint_as_float(a[REV ? 0 : 1]), __uint_as_float(u[REV ? 0 : 1]), A[c], U[c]);
+      if (!later) tot[w][ct * VEC + c] = float2{A[c], U[c]};
+      A[c] = later ? a0 : 1.f;
+      U[c] = later ? u0 : 0.f;
     }
   }
 }
