@@ -315,7 +315,7 @@ gdn2_status gdn2_norm_backward(const gdn2_norm_desc *d, const void *x, const voi
                                void *workspace, size_t workspace_bytes, void *stream) {
   const gdn2_status st = check_norm(d);
   if (st != GDN2_OK) return st;
-  const size_t ws = gdn2_norm_backward_workspace_bytes(d);
+  const size_t ws = dweight || dbias ? gdn2_norm_backward_workspace_bytes(d) : 0;
   if (ws > 0 && (!workspace || workspace_bytes < ws)) return GDN2_ERR_WORKSPACE;
   if (d->rows > 0 && (!x || !dy || !dx)) return GDN2_ERR_NULL_POINTER;
   if ((dweight && !weight) || (dbias && !bias) || (dgate && !gate)) return GDN2_ERR_NULL_POINTER;

@@ -291,15 +291,17 @@ def _autograd_function():
 
         @staticmethod
         def backward(ctx, dO, dh_T):
+            # autograd has made the forward's device and stream current
             no_second_order("gated_linear_recurrence")
             x, a, b, cu, h0, ck = ctx.saved_tensors
-            with launch_on(x.device, None) as handle:
-                dO = torch.zeros_like(x) if dO is None else dO.contiguous()
-                dh_T = None if dh_T is None else dh_T.contiguous()
-                empty = torch.empty_like
-                g = (empty(x), empty(a), None if b is None else empty(b), None if h0 is None else empty(h0))
-                _launch_backward(ctx.desc, x, a, b, cu, h0, ck, dO, dh_T, g, None, handle)
-            return g[0], g[1], g[2], None, g[3], None
+            empty = torch.empty_like
+            dO = torch.zeros_like(x) if dO is None else dO.contiguous()
+            dh_T = None if dh_T is None else dh_T.contiguous()
+            dx, da = empty(x), empty(a)
+            db, dh0 = None if b is None else empty(b), None if h0 is None else empty(h0)
+            _launch_backward(ctx.desc, x, a, b, cu, h0, ck, dO, dh_T, (dx, da, db, dh0), None,
+                             torch._C._cuda_getCurrentRawStream(x.device.index))
+            return dx, da, db, None, dh0, None
 
     return GatedLinearRecurrence
 

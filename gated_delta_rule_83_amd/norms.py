@@ -106,9 +106,11 @@ def norm_backward(x, weight, bias, gate, dy, eps: float = 1e-5, kind: str = "lay
 
 def _launch_backward(desc, x, weight, bias, gate, dy, g, workspace, handle):
     """A checked problem, on its device and stream; g: dx, dweight, dbias, dgate."""
-    work = _scratch(workspace, gdn2_norm_backward_workspace_bytes(desc), x.device)
-    st = gdn2_norm_backward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), *map(_ptr, g), _ptr(work),
-                            work.numel() if work is not None else 0, handle)
+    dx, dw, db, dz = g
+    need = gdn2_norm_backward_workspace_bytes(desc) if dw is not None or db is not None else 0
+    work = _scratch(workspace, need, x.device)
+    st = gdn2_norm_backward(desc, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(db),
+                            _ptr(dz), _ptr(work), work.numel() if work is not None else 0, handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
 
@@ -133,15 +135,16 @@ def _autograd_function():
 
         @staticmethod
         def backward(ctx, dy):
+            # autograd has made the forward's device and stream current
             no_second_order("norm")
             x, weight, bias, gate = ctx.saved_tensors
-            need = ctx.needs_input_grad
-            with launch_on(x.device, None) as handle:
-                empty = torch.empty_like
-                g = (empty(x), empty(weight) if need[1] else None, empty(bias) if need[2] else None,
-                     empty(gate) if need[3] else None)
-                _launch_backward(ctx.desc, x, weight, bias, gate, dy.contiguous(), g, None, handle)
-            return g + (None, None)
+            _, need_w, need_b, need_g, _, _ = ctx.needs_input_grad
+            desc, empty = ctx.desc, torch.empty_like
+            dx = empty(x)
+            dw, db, dz = empty(weight) if need_w else None, empty(bias) if need_b else None, empty(gate) if need_g else None
+            _launch_backward(desc, x, weight, bias, gate, dy.contiguous(), (dx, dw, db, dz), None,
+                             torch._C._cuda_getCurrentRawStream(x.device.index))
+            return dx, dw, db, dz, None, None
 
     return GatedNorm
 

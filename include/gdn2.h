@@ -570,7 +570,8 @@ gdn2_status gdn2_norm_forward(const gdn2_norm_desc *desc, const void *x, const v
  *       order, or NULL (required NULL without a weight or bias). rows == 0
  *       gives zeros.
  * workspace: gdn2_norm_backward_workspace_bytes(desc) bytes, 16-byte aligned:
- * partial sums of the weight's and the bias's gradient. */
+ * partial sums of the weight's and the bias's gradient (not used where neither
+ * is wanted). */
 size_t gdn2_norm_backward_workspace_bytes(const gdn2_norm_desc *desc);
 gdn2_status gdn2_norm_backward(const gdn2_norm_desc *desc, const void *x, const void *weight, const void *bias,
                                const void *gate, const void *dy, void *dx, void *dweight, void *dbias, void *dgate,
