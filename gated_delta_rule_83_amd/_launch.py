@@ -11,7 +11,7 @@ def want(t, name, shape, dtype, device):
     if t is None:
         return
     try:
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
             return
     except AttributeError:
         pass
@@ -41,10 +41,11 @@ class launch_on:
         import torch
         s = self._stream
         if s is None:
-            if torch.cuda.current_device() != self._dev.index:
+            index = self._dev.index
+            if torch._C._cuda_getDevice() != index:
                 self._ctx = torch.cuda.device(self._dev)
                 self._ctx.__enter__()
-            return torch._C._cuda_getCurrentRawStream(self._dev.index)
+            return torch._C._cuda_getCurrentRawStream(index)
         if not hasattr(s, "cuda_stream"):
             s = (torch.cuda.ExternalStream(int(s), device=self._dev) if int(s)
                  else torch.cuda.default_stream(self._dev))

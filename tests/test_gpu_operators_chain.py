@@ -165,3 +165,22 @@ def test_a_captured_training_step():
         got = [t.clone() for t in out]
         for u, v in zip(got, step()):
             assert torch.equal(u, v), i
+
+
+def test_calls_at_once_on_two_streams():
+    """Chained recurrences of different sizes side by side: every call gives the bits it gives alone."""
+    mk = lambda B, T, D: [torch.randn(B, T, D, device=DEV), torch.rand(B, T, D, device=DEV), torch.rand(B, T, D, device=DEV)]
+    p, q = mk(1, 20000, 256), mk(3, 3000, 640)
+    dO = torch.randn_like(q[0])
+    alone = [g.linear_forward(*p)[0], *g.linear_backward(*q, None, dO).values()]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(5):
+        got = []
+        for _ in range(3):
+            with torch.cuda.stream(s1):
+                got.append((g.linear_forward(*p)[0], alone[0]))
+            with torch.cuda.stream(s2):
+                got += list(zip(g.linear_backward(*q, None, dO).values(), alone[1:]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in got), i
