@@ -265,14 +265,18 @@ __device__ __forceinline__ void take_tile(const Chain &ch, int *slot, int tid, i
   }
 }
 
-// The value entering tile k of its chain, for this thread's channel in the first kLinChannels threads
-// (start: the value entering the chain), from the tiles' published maps; own:
-// this tile's map. Publishes both. Every thread of the workgroup calls it.
+// The value entering tile k of its chain, for this thread's channel in the
+// first kLinChannels threads, from the tiles' published maps; own: this tile's
+// map. Publishes both. Every thread of the workgroup calls it. start: the value
+// entering the chain, in its first tile (0 in others). That tile publishes the
+// value leaving it as a map with A = 0, so that no other one reads where start
+// lies: the chain's last value may be written there.
 template <bool CUT>
 __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 own, float start,
                                       float2 (*maps)[kLinChannels], int tid) {
   const int lane = tid % kLinChannels, w = tid / kLinChannels, in = k % kGroup;
   if (ch.tiles == 1) return start;
+  if (k == 0) own = float2{0.f, apply<CUT>(own.x, own.y, start)};
   if (w == 0 && in != kGroup - 1 && k != ch.tiles - 1)
     __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * kLinChannels + lane,
                        (uint64_t)word(own.x) | (uint64_t)word(own.y) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -288,7 +292,8 @@ __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 
     for (int j = 0; j < kGroup / kTeams; ++j) {
       v[j] = 0;
       if (kTeams * j + w < in)
-        v[j] = __hip_atomic_load(at + (size_t)kTeams * j * ch.chains * kLinChannels, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        v[j] = __hip_atomic_load(at + (size_t)kTeams * j * ch.chains * kLinChannels, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
       ready = ready && v[j] != ~(uint64_t)0;
     }
     if (ready) break;
@@ -311,8 +316,8 @@ __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 
   }
   h = apply<CUT>(A, U, h);
   if (in == kGroup - 1 && k != ch.tiles - 1)
-    __hip_atomic_store(ch.value + ((size_t)(k / kGroup) * ch.chains + chain) * kLinChannels + lane, word(apply<CUT>(own.x, own.y, h)),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(ch.value + ((size_t)(k / kGroup) * ch.chains + chain) * kLinChannels + lane,
+                       word(apply<CUT>(own.x, own.y, h)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return h;
 }
 
@@ -465,7 +470,7 @@ __global__ __launch_bounds__(kNT, VEC == 4 ? 4 : 1) void linear_forward_chain(Li
   __syncthreads();
   {
     const int c = blk * kLinChannels + lane;
-    const float start = !PACKED && p.h0 && c < D && tid < kLinChannels ? p.h0[(size_t)n * D + c] : 0.f;
+    const float start = !PACKED && k == 0 && p.h0 && c < D && tid < kLinChannels ? p.h0[(size_t)n * D + c] : 0.f;
     const float in = link<PACKED>(ch, k, chain, tile_map<G::PARTS, false, PACKED>(tot, lane), start, maps, tid);
     if (tid < kLinChannels) {
       entering[lane] = in;
@@ -648,7 +653,7 @@ __global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
   __syncthreads();
   {
     const int c = blk * kLinChannels + lane;
-    const float start = !PACKED && p.dh_T && c < D && tid < kLinChannels ? p.dh_T[(size_t)n * D + c] : 0.f;
+    const float start = !PACKED && k == 0 && p.dh_T && c < D && tid < kLinChannels ? p.dh_T[(size_t)n * D + c] : 0.f;
     const float in = link<PACKED>(ch, k, chain, tile_map<G::PARTS, true, PACKED>(tot[1], lane), start, maps, tid);
     if (tid < kLinChannels) entering[lane] = in;
   }
