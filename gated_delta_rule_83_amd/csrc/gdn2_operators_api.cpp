@@ -78,9 +78,9 @@ size_t linear_forward_ws(const gdn2_linear_desc *d, bool packed) {
 
 size_t linear_backward_ws(const gdn2_linear_desc *d, bool packed) {
   if (check_linear(d) != GDN2_OK) return 0;
-  return d->B == 0 ? 0
-                   : gdn2::linear_chain_bytes(d->B, d->T, d->D, packed) +
-                         gdn2::linear_checkpoint_rows(d->B, d->T, packed) * (size_t)d->D * 4;
+  if (d->B == 0 && !packed) return 0;
+  return gdn2::linear_chain_bytes(d->B, d->T, d->D, packed) +
+         gdn2::linear_checkpoint_rows(d->B, d->T, packed) * (size_t)d->D * 4;
 }
 
 gdn2_status linear_forward(const gdn2_linear_desc *d, bool packed, const int32_t *cu, const void *x, const void *a,
@@ -122,7 +122,7 @@ gdn2_status linear_backward(const gdn2_linear_desc *d, bool packed, const int32_
                             void *stream) {
   const gdn2_status st = check_linear(d);
   if (st != GDN2_OK) return st;
-  if (d->B == 0) return GDN2_OK;
+  if (d->B == 0 && (!packed || d->T == 0)) return GDN2_OK;  // packed tokens of no sequence: gradients of zero
   if (packed && !cu) return GDN2_ERR_NULL_POINTER;
   if (tied_gates(d->gates)) b = db = nullptr;
   const size_t ws = linear_backward_ws(d, packed);

@@ -137,6 +137,20 @@ def test_packed(lens, D, form, dtype):
     check(p, [(slice(cu[n], cu[n + 1]), n) for n in range(N)], form, keep, h, dict(again, dh0=d))
 
 
+@pytest.mark.parametrize("cu", [[70], [200, 200], [0, 0, 0]])
+def test_packed_tokens_of_no_sequence(cu):
+    """No sequence, or empty ones only: outputs left as they were, gradients zero, states passed through."""
+    f = dict(device=DEV, dtype=torch.float32)
+    x, n = torch.full((200, 12), float("nan"), **f), len(cu) - 1
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    h0, dhT = torch.randn(n, 12, **f), torch.randn(n, 12, **f)
+    o, h_T = g.linear_forward_varlen(x, x, x, cud, h0, o=torch.full_like(x, 7.0))
+    gr = g.linear_backward_varlen(x, x, x, cud, h0, x, dhT)
+    torch.cuda.synchronize()
+    assert (o == 7.0).all() and torch.equal(h_T, h0) and torch.equal(gr["dh0"], dhT)
+    assert all((gr[k] == 0).all() for k in ("dx", "da", "db"))
+
+
 @pytest.mark.parametrize("D", [5, 64])
 def test_a_bad_sequence_stays_alone(D):
     """NaN and infinities of one packed sequence reach no other one, forward and backward."""

@@ -102,6 +102,8 @@ def test_empty_batches_return_before_any_pointer_check():
     assert fwd(lin(B=0), [0] * 7, ws=False) == g.GDN2_OK
     assert fwd_varlen(lin(B=0), [0] * 8) == g.GDN2_OK
     assert bwd(lin(B=0), [0] * 11, 0) == g.GDN2_OK
+    assert g.gdn2_linear_backward_varlen(lin(B=0, T=0), *[0] * 12) == g.GDN2_OK
+    assert g.gdn2_linear_backward_varlen(lin(B=0), *[0] * 12) == g.GDN2_ERR_NULL_POINTER  # zeros to write
     assert g.gdn2_linear_step(lin(B=0, T=1), *[0] * 6) == g.GDN2_OK
     assert g.gdn2_norm_forward(nrm(rows=0), 0, 0, 0, 0, 0) == g.GDN2_OK
     assert g.gdn2_state_cache_store(cch(N=0), 0, 0, 0, 0) == g.GDN2_OK
