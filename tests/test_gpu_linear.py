@@ -137,6 +137,26 @@ def test_packed(lens, D, form, dtype):
     check(p, [(slice(cu[n], cu[n + 1]), n) for n in range(N)], form, keep, h, dict(again, dh0=d))
 
 
+@pytest.mark.parametrize("form,dtype", [("preact", "bf16"), ("channel", "f32")])
+def test_more_workgroups_than_run_at_once(form, dtype):
+    """13 tiles, the last one short, of 168 chains, 25 of 84: batched and packed."""
+    T, D = 64 * 12 + 5, 128 * 83 + 60
+    p = problem(np.random.default_rng(79), (2, T), D, 2, form, dtype)
+    o, h_T, ck = g.linear_forward(p["x"], p["a"], p["b"], p["h0"], want_checkpoints=True, gates=form)
+    gr = g.linear_backward(p["x"], p["a"], p["b"], p["h0"], p["dO"], p["dhT"], ck=ck, gates=form)
+    torch.cuda.synchronize()
+    check(p, [(0, 0), (1, 1)], form, o, h_T, gr)
+    del o, ck, gr
+    cu = [0, 3, 700, 700, 2 * T]  # the same tokens as three sequences and an empty one: 25 tiles
+    q = dict({k: None if p[k] is None else p[k].flatten(0, 1) for k in ("x", "a", "b", "dO")},
+             h0=p["h0"].repeat(2, 1), dhT=p["dhT"].repeat(2, 1))
+    cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    o, h_T = g.linear_forward_varlen(q["x"], q["a"], q["b"], cud, q["h0"], gates=form)
+    gr = g.linear_backward_varlen(q["x"], q["a"], q["b"], cud, q["h0"], q["dO"], q["dhT"], gates=form)
+    torch.cuda.synchronize()
+    check(q, [(slice(cu[n], cu[n + 1]), n) for n in range(4)], form, o, h_T, gr)
+
+
 @pytest.mark.parametrize("cu", [[70], [200, 200], [0, 0, 0]])
 def test_packed_tokens_of_no_sequence(cu):
     """No sequence, or empty ones only: outputs left as they were, gradients zero, states passed through."""
