@@ -162,8 +162,8 @@ gdn2_status check_norm(const gdn2_norm_desc *d) {
     return GDN2_ERR_BAD_DTYPE;
   if (d->rows < 0 || d->D < 1 || !(d->eps >= 0.f) || isinf(d->eps)) return GDN2_ERR_BAD_SHAPE;
   if (d->kind != GDN2_NORM_LAYER && d->kind != GDN2_NORM_RMS) return GDN2_ERR_UNSUPPORTED;
-  // the columns are indexed in 32 bits, with a workgroup's stride past the end
-  if (d->D > INT32_MAX - 65536 || (uint64_t)d->rows > (uint64_t)INT64_MAX / 8 / (uint64_t)d->D)
+  // the columns' sums are one launch of a workgroup of 1024 threads for 16 columns
+  if (d->D > 1 << 25 || (uint64_t)d->rows > (uint64_t)INT64_MAX / 8 / (uint64_t)d->D)
     return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;
 }

@@ -544,8 +544,8 @@ gdn2_status gdn2_linear_backward_varlen(const gdn2_linear_desc *desc, const int3
  *
  *   x, gate, y : [rows, D] in desc->dtype; gate may be NULL (no factor)
  *   weight, bias : [D] in desc->wdtype; either may be NULL (ones, zeros)
- * Any rows >= 0, D >= 1; eps >= 0. Sums are fp32 (magnitudes above about 1e18
- * overflow the mean square). Tensors need only be aligned
+ * Any rows >= 0, D >= 1 up to 2^25 (GDN2_ERR_UNSUPPORTED past it); eps >= 0.
+ * Sums are fp32 (magnitudes above about 1e18 overflow the mean square). Tensors need only be aligned
  * to their elements; where D is a multiple of 8 and they are 16-byte aligned,
  * rows are moved with wide loads. */
 typedef enum { GDN2_NORM_LAYER = 0, GDN2_NORM_RMS = 1 } gdn2_norm_kind;

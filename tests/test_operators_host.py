@@ -118,7 +118,8 @@ def nrm(rows=100, D=128, kind=0, dtype=1, wdtype=0, eps=1e-5):
 BAD_NORM = [(None, g.GDN2_ERR_NULL_POINTER), (nrm(dtype=2), g.GDN2_ERR_BAD_DTYPE), (nrm(wdtype=-1), g.GDN2_ERR_BAD_DTYPE),
             (nrm(rows=-1), g.GDN2_ERR_BAD_SHAPE), (nrm(D=0), g.GDN2_ERR_BAD_SHAPE), (nrm(eps=-1.0), g.GDN2_ERR_BAD_SHAPE),
             (nrm(eps=float("nan")), g.GDN2_ERR_BAD_SHAPE), (nrm(eps=float("inf")), g.GDN2_ERR_BAD_SHAPE),
-            (nrm(kind=2), g.GDN2_ERR_UNSUPPORTED), (nrm(rows=2 ** 62), g.GDN2_ERR_UNSUPPORTED)]
+            (nrm(kind=2), g.GDN2_ERR_UNSUPPORTED), (nrm(rows=2 ** 62), g.GDN2_ERR_UNSUPPORTED),
+            (nrm(D=2 ** 25 + 1), g.GDN2_ERR_UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("desc,status", BAD_NORM)
