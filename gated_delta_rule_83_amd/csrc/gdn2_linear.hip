@@ -26,9 +26,9 @@ constexpr int kStepNT = 256;
 // Token tensors are read with nontemporal loads (load_raw). A pass over the
 // bytes of the forward in tiles, bf16, 32768 x 2048: with tiles of 64 channels
 // 5.2 TB/s without them and 5.6 to 6.2 with them, with tiles of 128 channels
-// (rows of 256 bytes) 6.3 TB/s. (In the whole kernel 128 channels by 64 tokens
-// took 114 us where 64 by 128 took 124, 256 by 32 took 119, and 512 threads
-// with 128 by 128 took 154.)
+// (rows of 256 bytes) 6.3 TB/s. (In the whole kernel 64 channels by 128 tokens
+// took 8% longer than 128 by 64, 256 by 32 took 4%, and 512 threads with 128
+// by 128 took 35%.)
 
 // 1 / (1 + e^x). e^x may be infinite (0). EXACT (fp32 pre-activations): the
 // reciprocal's error of one step taken out by a Newton step, x above 87 as 87
@@ -75,7 +75,7 @@ __device__ __forceinline__ void unpack_pair(float v, float &p, float &q) {
 // b) and the other factor its difference from 1: p (1 - p) is off by at most
 // 2^-24, which a bf16 gradient shows only where p is within 2^-15 of 0 (a) or
 // of 1 (b); unpacking pairs made that kernel bound by its arithmetic
-// (B1 T65536 D2048: 512 us against 445).
+// (B1 T65536 D2048: 15% slower).
 template <int FORM, bool EXACT> struct Gates {
   static __device__ __forceinline__ void pack(float &a, float &b) {
     if constexpr (Form<FORM>::pre) {
