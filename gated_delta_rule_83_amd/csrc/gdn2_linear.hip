@@ -516,9 +516,12 @@ __global__ __launch_bounds__(kNT, VEC == 4 ? 4 : 1) void linear_forward_chain(Li
 }
 
 // The gradients, tile by tile from the last one: the adjoint is chained, the
-// states come from the saved ones.
+// states come from the saved ones. Two waves a SIMD: fp32 with untied gates and
+// packed single values would take a few registers past the half of them (B4
+// T4096 D2048 fp32 pre-activations 250 us instead of 202, packed 16384 x 1001
+// bf16 pre-activations 152 instead of 103).
 template <bool BF16, int FORM, int VEC, bool PACKED>
-__global__ __launch_bounds__(kNT) void linear_backward_chain(Lin p, Chain ch) {
+__global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
   constexpr bool GB = BF16 && Form<FORM>::pre;
   __shared__ float2 tot[2][G::PARTS][kLinChannels], maps[kGroup][kLinChannels];
