@@ -37,12 +37,20 @@ __device__ __forceinline__ void store_w(void *p, int i, bool bf16, float v) {
     static_cast<float *>(p)[i] = v;
 }
 
-// 1 / (1 + e^-z); z below -87 counts as -87 (2e-38), NaN stays.
-__device__ __forceinline__ float sigmoid(float z) {
-  z = z < -87.f ? -87.f : z;
+// s = 1 / (1 + e^-z) of a gate z. Below -87 (s is 2e-38 there) a gate is closed:
+// s is 0 and z comes back as -87, so that z s and its derivative are 0 however
+// low z is, -inf too. NaN stays.
+__device__ __forceinline__ float sigmoid(float &z) {
+  const bool closed = z < -87.f;
+  z = closed ? -87.f : z;
   const float d = 1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f);
   const float r = __builtin_amdgcn_rcpf(d);
-  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  return closed ? 0.f : __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+}
+// The derivative of z s from it and s; s is 1 long before z s is 88, so 88 stands
+// for all above it (inf * 0).
+__device__ __forceinline__ float silu_slope(float zs, float s) {
+  return __builtin_fmaf(__builtin_fminf(zs, 88.f), 1.f - s, s);
 }
 
 // ------------------------------------------------------------------ rows in registers
@@ -123,14 +131,18 @@ __device__ __forceinline__ void load_row(Raw<BF16, V> (&x)[C::NC], const void *p
   }
 }
 
+// Piece j of a lane's row.
+template <bool BF16, int V, class C>
+__device__ __forceinline__ void store_piece(void *p, int64_t row, int j, const NormArgs &a, int l, const float (&y)[V]) {
+  char *base = static_cast<char *>(p) + (size_t)row * a.D * sizeof(typename Elem<BF16>::T);
+  const int col = (j * C::lanes() + l) * V;
+  if (col < a.D) store_at<BF16>(base + col * (uint32_t)sizeof(typename Elem<BF16>::T), y);
+}
+
 template <bool BF16, int V, class C>
 __device__ __forceinline__ void store_row(void *p, int64_t row, const NormArgs &a, int l, const float (&y)[C::NC][V]) {
-  char *base = static_cast<char *>(p) + (size_t)row * a.D * sizeof(typename Elem<BF16>::T);
 #pragma unroll
-  for (int j = 0; j < C::NC; ++j) {
-    const int col = (j * C::lanes() + l) * V;
-    if (col < a.D) store_at<BF16>(base + col * (uint32_t)sizeof(typename Elem<BF16>::T), y[j]);
-  }
+  for (int j = 0; j < C::NC; ++j) store_piece<BF16, V, C>(p, row, j, a, l, y[j]);
 }
 
 template <int V, class C>
@@ -180,8 +192,9 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
       for (int v = 0; v < V; ++v) {
         c[j][v] = __builtin_fmaf(c[j][v] * r, w[j][v], b[j][v]);
         if constexpr (GATE) {
-          const float zv = z[j][v];
-          c[j][v] *= zv * sigmoid(zv);
+          float zv = z[j][v];
+          const float sg = sigmoid(zv);
+          c[j][v] *= zv * sg;
         }
       }
     }
@@ -223,18 +236,19 @@ template <bool BF16, bool GATE, int V, class C> __global__ __launch_bounds__(C::
     float c[NC][V], d[NC][V], r, s[2] = {0.f, 0.f};
     centre<BF16, C, V>(c, r, x, one, p, inv, red[par], tid);
     if constexpr (GATE) {
-      float dz[NC][V];
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
+        float dz[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float zv = z[j][v], sg = sigmoid(zv), yv = y[j][v];
+          float zv = z[j][v];
+          const float sg = sigmoid(zv), zs = zv * sg, yv = y[j][v];
           const float n = __builtin_fmaf(c[j][v] * r, w[j][v], b[j][v]);
-          dz[j][v] = yv * n * (sg * __builtin_fmaf(zv, 1.f - sg, 1.f));
-          d[j][v] = yv * (zv * sg);
+          dz[v] = yv * n * silu_slope(zs, sg);
+          d[j][v] = yv * zs;
         }
+        if (p.dgate) store_piece<BF16, V, C>(p.dgate, row, j, p, l, dz);
       }
-      if (p.dgate) store_row<BF16, V, C>(p.dgate, row, p, l, dz);
     } else {
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
@@ -341,7 +355,10 @@ template <bool BF16, bool GATE, int V> __global__ __launch_bounds__(kBlock) void
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         f[v] = (f[v] - mean) * r * load_w(p.weight, c + v, p.wbf16, 1.f) + load_w(p.bias, c + v, p.wbf16, 0.f);
-        if constexpr (GATE) f[v] *= z[v] * sigmoid(z[v]);
+        if constexpr (GATE) {
+          const float sg = sigmoid(z[v]);
+          f[v] *= z[v] * sg;
+        }
       }
       store_f<BF16>(p.y, (size_t)row * p.D + c, f);
     }
@@ -373,8 +390,9 @@ template <bool BF16, bool GATE, int V> __global__ __launch_bounds__(kBlock) void
         const float w = load_w(p.weight, c + v, p.wbf16, 1.f);
         if constexpr (GATE) {
           const float sg = sigmoid(z[v]), n = f[v] * w + load_w(p.bias, c + v, p.wbf16, 0.f), dz = d[v] * n;
-          d[v] *= z[v] * sg;
-          z[v] = dz * (sg * (1.f + z[v] * (1.f - sg)));
+          const float zs = z[v] * sg;
+          d[v] *= zs;
+          z[v] = dz * silu_slope(zs, sg);
         }
         s[0] += d[v] * w;
         s[1] += d[v] * w * f[v];
@@ -403,7 +421,10 @@ template <bool BF16, bool GATE, int V> __global__ __launch_bounds__(kBlock) void
       if constexpr (GATE) load_f<BF16>(z, p.gate, at + c);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if constexpr (GATE) d[v] *= z[v] * sigmoid(z[v]);
+        if constexpr (GATE) {
+          const float sg = sigmoid(z[v]);
+          d[v] *= z[v] * sg;
+        }
         d[v] = r * (d[v] * load_w(p.weight, c + v, p.wbf16, 1.f) - (f[v] - mean) * r * mx - md);
       }
       store_f<BF16>(p.dx, at + c, d);

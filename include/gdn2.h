@@ -542,7 +542,9 @@ gdn2_status gdn2_linear_backward_varlen(const gdn2_linear_desc *desc, const int3
  *   c = x - mean(x) (GDN2_NORM_LAYER) or x (GDN2_NORM_RMS)
  *   y = (c / sqrt(mean(c^2) + eps) * weight + bias) * silu(gate)
  *
- *   x, gate, y : [rows, D] in desc->dtype; gate may be NULL (no factor)
+ *   x, gate, y : [rows, D] in desc->dtype; gate may be NULL (no factor). A gate
+ *                below -87 (-inf too) is closed: silu and its derivative, 1.5e-36
+ *                there, count as 0. Far above 0 the derivative is 1 (+inf too).
  *   weight, bias : [D] in desc->wdtype; either may be NULL (ones, zeros)
  * Any rows >= 0, D >= 1 up to 2^25 (GDN2_ERR_UNSUPPORTED past it); eps >= 0.
  * Sums are fp32 (magnitudes above about 1e18 overflow the mean square). Tensors need only be aligned

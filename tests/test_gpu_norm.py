@@ -206,3 +206,55 @@ def test_offsets_past_32_bits():
     torch.cuda.synchronize()
     assert (y[:-4] == 0).all() and (gr["dx"][:-4] == 0).all()
     check(p, "layer", float(np.float32(1e-5)), y[-4:], dict(gr, dx=gr["dx"][-4:]))
+
+
+def closed(z):
+    """The gate as the header defines it: below -87 its factor silu(gate) is 0 (1.5e-36 at -87), and so is its derivative."""
+    return torch.where(z.double() < -87.0, torch.full_like(z, -1e4, dtype=torch.float64), z.double())
+
+
+# one row plan each: lanes of a wave with wide, 8-byte and single loads, workgroups with one, two and four pieces a
+# lane, and rows past the registers with vectors and single values
+FAR = [(9, 128), (9, 500), (9, 137), (6, 1024), (6, 2052), (5, 1001), (3, 8192), (3, 16392), (3, 5001)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,bias", [("layer", True), ("rms", False)])
+@pytest.mark.parametrize("rows,D", FAR)
+def test_closed_gates(rows, D, kind, bias, dtype):
+    """Gates far below 0, the type's lowest value and -inf among them, close their channels: nothing of them is left
+    in the result or in any gradient, and the other channels are what they are without them."""
+    p = problem(np.random.default_rng(rows + D), (rows, D), dtype, "f32", bias, True)
+    low = torch.finfo(R.TORCH[dtype]).min
+    far = torch.tensor([-70.0, -88.0, -100.0, -104.0, -1e4, -1e30, -1e36, low, -float("inf")], device=DEV)
+    at = torch.arange(0, D, 5, device=DEV)
+    p["z"][:, at] = far[torch.arange(len(at), device=DEV) % len(far)].to(p["z"].dtype)
+    p["z"][1] = low  # a row whose gate leaves nothing
+    y = g.norm_forward(p["x"], p["w"], p["b"], p["z"], kind=kind)
+    gr = g.norm_backward(p["x"], p["w"], p["b"], p["z"], p["dy"], kind=kind)
+    torch.cuda.synchronize()
+    shut = p["z"].float() < -87.0
+    assert (y[shut] == 0).all() and (gr["dgate"][shut] == 0).all()
+    assert (y[1] == 0).all() and (gr["dx"][1] == 0).all() and (gr["dgate"][1] == 0).all()
+    check(dict(p, z=closed(p["z"])), kind, float(np.float32(1e-5)), y, gr)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [128, 137, 1024, 1001, 16392, 5001])
+def test_open_gates(D, dtype):
+    """Gates far above 0: silu(gate) is the gate and its derivative 1, for +inf too."""
+    p = problem(np.random.default_rng(D), (3, D), dtype, "f32", True, True)
+    for i, v in enumerate((100.0, 1e30, float("inf"))):
+        p["z"][i, ::7] = v
+    y = g.norm_forward(p["x"], p["w"], p["b"], p["z"])
+    gr = g.norm_backward(p["x"], p["w"], p["b"], p["z"], p["dy"])
+    torch.cuda.synchronize()
+    n = R.norm(R.f64(p["x"]), R.f64(p["w"]), R.f64(p["b"]), None, float(np.float32(1e-5)), "layer")[:, ::7]
+    # n: its mean's, root's and own roundings as in check, at most 4 K of its terms' size, 1 + |w| + |b| + |n| here
+    tol = 4 * (D / 64 + 10) * R.U32 * (1 + np.abs(n) + np.abs(R.f64(p["w"]))[::7] + np.abs(R.f64(p["b"]))[::7])
+    half, dy = 0.0 if dtype == "f32" else R.half(R.TORCH[dtype]), R.f64(p["dy"])[:, ::7]
+    assert (np.abs(R.f64(gr["dgate"])[:, ::7] - dy * n) <= np.abs(dy) * tol + (half + 4 * R.U32) * np.abs(dy) * (np.abs(n) + tol)).all()
+    z = R.f64(p["z"])[:2, ::7]
+    assert (np.abs(R.f64(y)[:2, ::7] - n[:2] * z) <= np.abs(z) * (tol + (half + 4 * R.U32) * (np.abs(n) + tol))[:2]).all()
+    sure = np.abs(n[2]) > tol[2]
+    assert (R.f64(y)[2, ::7][sure] == (np.sign(n[2]) * np.inf)[sure]).all()
