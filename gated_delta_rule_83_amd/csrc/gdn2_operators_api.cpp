@@ -44,17 +44,18 @@ gdn2_status check_overlap(const Range *in, int ni, const Range *out, int no, con
 }
 
 // ------------------------------------------------------------------ linear recurrence
-gdn2_status check_linear(const gdn2_linear_desc *d) {
+gdn2_status check_linear(const gdn2_linear_desc *d, bool packed) {
   if (!d) return GDN2_ERR_NULL_POINTER;
   if (d->dtype != GDN2_F32 && d->dtype != GDN2_BF16) return GDN2_ERR_BAD_DTYPE;
   if (d->B < 0 || d->T < 0 || d->D < 1) return GDN2_ERR_BAD_SHAPE;
   if (d->gates < GDN2_LINEAR_CHANNEL || d->gates > GDN2_LINEAR_TIED_PREACT) return GDN2_ERR_UNSUPPORTED;
   // a tile's 128 token rows are addressed with 32-bit offsets
   if (d->T > INT32_MAX - 256 || d->D > 1 << 22) return GDN2_ERR_UNSUPPORTED;
-  // both are below 2^25 * 2^24 where the product is formed
+  // workgroups: a tile of a chain each, and of whole sequences each has its own
+  // chains; the products are below 2^25 * 2^15 and 2^24 * 2^31
   const size_t tiles = ceil_div((size_t)d->T, gdn2::kLinTile), blocks = ceil_div((size_t)d->D, gdn2::kLinChannels);
-  const size_t per = (tiles > 0 ? tiles : 1) * blocks;
-  if (per > kMaxGroups || (d->B > 0 && per * (size_t)d->B > kMaxGroups)) return GDN2_ERR_UNSUPPORTED;
+  const size_t per = (tiles > 0 ? tiles : 1) * blocks, B = (size_t)d->B;
+  if (per > kMaxGroups || (packed ? B : per * B) > kMaxGroups) return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;
 }
 
@@ -72,12 +73,12 @@ bool tied_gates(int g) { return g == GDN2_LINEAR_TIED || g == GDN2_LINEAR_TIED_P
 bool pre_gates(int g) { return g == GDN2_LINEAR_PREACT || g == GDN2_LINEAR_TIED_PREACT; }
 
 size_t linear_forward_ws(const gdn2_linear_desc *d, bool packed) {
-  if (check_linear(d) != GDN2_OK) return 0;
+  if (check_linear(d, packed) != GDN2_OK) return 0;
   return d->B == 0 ? 0 : gdn2::linear_chain_bytes(d->B, d->T, d->D, packed);
 }
 
 size_t linear_backward_ws(const gdn2_linear_desc *d, bool packed) {
-  if (check_linear(d) != GDN2_OK) return 0;
+  if (check_linear(d, packed) != GDN2_OK) return 0;
   if (d->B == 0 && !packed) return 0;
   return gdn2::linear_chain_bytes(d->B, d->T, d->D, packed) +
          gdn2::linear_checkpoint_rows(d->B, d->T, packed) * (size_t)d->D * 4;
@@ -86,7 +87,7 @@ size_t linear_backward_ws(const gdn2_linear_desc *d, bool packed) {
 gdn2_status linear_forward(const gdn2_linear_desc *d, bool packed, const int32_t *cu, const void *x, const void *a,
                            const void *b, const float *h0, void *o, float *h_T, float *ck, void *workspace,
                            size_t workspace_bytes, void *stream) {
-  const gdn2_status st = check_linear(d);
+  const gdn2_status st = check_linear(d, packed);
   if (st != GDN2_OK) return st;
   if (d->B == 0) return GDN2_OK;
   if (packed && !cu) return GDN2_ERR_NULL_POINTER;
@@ -120,7 +121,7 @@ gdn2_status linear_backward(const gdn2_linear_desc *d, bool packed, const int32_
                             const void *b, const float *h0, const float *ck, const void *dO, const float *dh_T,
                             void *dx, void *da, void *db, float *dh0, void *workspace, size_t workspace_bytes,
                             void *stream) {
-  const gdn2_status st = check_linear(d);
+  const gdn2_status st = check_linear(d, packed);
   if (st != GDN2_OK) return st;
   if (d->B == 0 && (!packed || d->T == 0)) return GDN2_OK;  // packed tokens of no sequence: gradients of zero
   if (packed && !cu) return GDN2_ERR_NULL_POINTER;
@@ -249,7 +250,7 @@ gdn2_status gdn2_linear_forward_varlen(const gdn2_linear_desc *d, const int32_t 
 
 gdn2_status gdn2_linear_step(const gdn2_linear_desc *d, const void *x, const void *a, const void *b, const float *h,
                              float *h_out, void *o, void *stream) {
-  const gdn2_status st = check_linear(d);
+  const gdn2_status st = check_linear(d, false);
   if (st != GDN2_OK) return st;
   if (d->T != 1) return GDN2_ERR_BAD_SHAPE;
   if (d->B == 0) return GDN2_OK;

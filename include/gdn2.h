@@ -446,8 +446,9 @@ gdn2_status gdn2_chunk_backward_varlen_gates(const gdn2_desc *desc, const int32_
  *   a, b      : [B, T, D], by gate form (below)
  *   h0, h_T   : [B, D] fp32
  * Any B, T >= 0 and D >= 1; T <= 2^31 - 257, D <= 2^22 and B * ceil(T / 64) *
- * ceil(D / 128) <= 2^24 - 1 (GDN2_ERR_UNSUPPORTED beyond). Where D is a
- * multiple of 4 and every tensor 16-byte aligned, rows are moved with wide loads.
+ * ceil(D / 128) <= 2^24 - 1, for packed sequences ceil(T / 64) * ceil(D / 128)
+ * and B each (GDN2_ERR_UNSUPPORTED beyond). Where D is a multiple of 4 and every
+ * tensor 16-byte aligned, rows are moved with wide loads.
  *
  * Gate forms:
  *   GDN2_LINEAR_CHANNEL     : a decay, b input gate, fp32

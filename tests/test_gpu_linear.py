@@ -373,3 +373,21 @@ def test_offsets_past_32_bits():
     close("dx", gr["dx"][sl], dx, np.abs(ad).max(), torch.bfloat16)
     close("da", gr["da"][sl], da, np.abs(ad).max() * 2 * np.abs(R.f64(x[sl])).max(), torch.bfloat16, 2.0)
     assert (gr["dx"][0] == 0).all()
+
+
+def test_more_sequences_than_workgroups():
+    """6000 sequences of 0 to 5 tokens at a width where each has 32 blocks of channels: batches of single tokens and
+    short prompts as a server packs them."""
+    rng = np.random.default_rng(31)
+    lens = rng.integers(0, 6, 6000)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T, D, N = int(cu[-1]), 4096, 6000
+    p = problem(rng, (T,), D, N, "preact", "bf16")
+    cud = torch.tensor(cu, device=DEV)
+    o, h_T, ck = g.linear_forward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], want_checkpoints=True, gates="preact")
+    gr = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], p["dO"], p["dhT"], ck=ck, gates="preact")
+    torch.cuda.synchronize()
+    some = [0, 1, 2, 3000, 3001, 5998, 5999] + list(np.argwhere(lens == 0)[:5, 0]) + list(rng.integers(0, N, 20))
+    check(p, [(slice(cu[n], cu[n + 1]), n) for n in some], "preact", o, h_T, gr)
+    empty = torch.tensor(lens == 0, device=DEV)
+    assert torch.equal(h_T[empty], p["h0"][empty]) and torch.equal(gr["dh0"][empty], p["dhT"][empty])

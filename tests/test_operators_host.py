@@ -303,3 +303,19 @@ def test_structures_match_the_header():
     """Field sizes as the C compiler lays them out: five or five 32-bit fields, and a 64-bit one first."""
     assert ctypes.sizeof(g.gdn2_linear_desc) == 20 and ctypes.sizeof(g.gdn2_cache_desc) == 20
     assert ctypes.sizeof(g.gdn2_norm_desc) == 32 and g.gdn2_norm_desc.eps.offset == 24
+
+
+def test_packed_limits_do_not_count_sequences():
+    """A packed call's workgroups come from its tokens and channels; B sequences only make B + 1 offsets and B states."""
+    queries = (g.gdn2_linear_forward_varlen_workspace_bytes, g.gdn2_linear_backward_varlen_workspace_bytes)
+    for d in (lin(B=512, T=65536, D=4096), lin(B=4096, T=8192, D=4096), lin(B=2 ** 24 - 1, T=8192, D=4096),
+              lin(B=2 ** 24 - 1, T=64 * (2 ** 24 - 1), D=128), lin(B=2 ** 24 - 1, T=0, D=2 ** 22)):
+        assert (d.T == 0) == (queries[0](d) == 0)
+        # accepted as a description: the missing offsets are the first thing wrong with the call
+        assert fwd_varlen(d, put(fakes(8), _0=0)) == g.GDN2_ERR_NULL_POINTER
+        assert g.gdn2_linear_backward_varlen(d, 0, *fakes(11), FAKE - EACH, 1 << 30, 0) == g.GDN2_ERR_NULL_POINTER
+        assert fwd(d) == g.GDN2_ERR_UNSUPPORTED and bwd(d) == g.GDN2_ERR_UNSUPPORTED  # as whole sequences: too many
+    assert queries[1](lin(B=4096, T=8192, D=4096)) == queries[1](lin(B=1, T=8192, D=4096))
+    for d in (lin(B=2 ** 24, T=64), lin(B=1, T=64 * (2 ** 24 - 1) + 1, D=128), lin(B=1, T=64 * (2 ** 24 - 1), D=129),
+              lin(B=2 ** 31 - 1, T=1, D=1)):
+        assert fwd_varlen(d) == g.GDN2_ERR_UNSUPPORTED and queries[0](d) == queries[1](d) == 0
