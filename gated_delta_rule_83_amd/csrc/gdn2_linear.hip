@@ -728,6 +728,10 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
   if (!PACKED && p.dh0 && tile == 0 && own && s == 0) store_f<false>(p.dh0, (size_t)n * D + c0, m);
 }
 
+// Channels of a state that a workgroup passes on at a time, and such pieces of a state.
+constexpr int kPass = 4096;
+__host__ __device__ inline uint32_t pass_pieces(int D) { return (uint32_t)(D + kPass - 1) / kPass; }
+
 // Before a chained launch: the words not published yet, and what needs no
 // token: the states of empty sequences pass through (all of them without cu).
 __global__ __launch_bounds__(kNT) void chain_prepare(uint4 *words, size_t count, const int32_t *cu, int B, int T, int D,
@@ -735,9 +739,12 @@ __global__ __launch_bounds__(kNT) void chain_prepare(uint4 *words, size_t count,
   const size_t me = (size_t)blockIdx.x * kNT + threadIdx.x;
   for (size_t i = me; i < count; i += (size_t)gridDim.x * kNT) words[i] = uint4{~0u, ~0u, ~0u, ~0u};
   if (!to) return;
-  for (int n = blockIdx.x; n < B; n += gridDim.x) {
+  const uint32_t per = pass_pieces(D);
+  for (size_t i = blockIdx.x; i < (size_t)B * per; i += gridDim.x) {
+    const int n = (int)(i / per), c0 = (int)(i - (size_t)n * per) * kPass;
     if (cu && clamp_offset(cu[n + 1], T) > clamp_offset(cu[n], T)) continue;
-    for (int c = threadIdx.x; c < D; c += kNT) to[(size_t)n * D + c] = from ? from[(size_t)n * D + c] : 0.f;
+    const int end = c0 + kPass < D ? c0 + kPass : D;
+    for (int c = c0 + threadIdx.x; c < end; c += kNT) to[(size_t)n * D + c] = from ? from[(size_t)n * D + c] : 0.f;
   }
 }
 
@@ -793,8 +800,10 @@ hipError_t launch_v(const LinearArgs &q, Op op, hipStream_t st) {
   const float *from = op == kForward ? q.h0 : q.dh_T;
   float *to = !q.cu && ch.tiles ? nullptr : op == kForward ? q.h_T : q.dh0;
   if (bytes || to) {
-    const size_t count = bytes / 16, wgs = (count + kNT - 1) / kNT;
-    const size_t grid = wgs < 1 ? 1 : wgs > 2048 ? 2048 : wgs;
+    // enough workgroups for the words and for the states (64 tokens among 4096
+    // sequences of 4096 channels: 16 ms with one)
+    const size_t count = bytes / 16, wgs = (count + kNT - 1) / kNT, pass = to ? (size_t)q.B * pass_pieces(q.D) : 0;
+    const size_t most = wgs > pass ? wgs : pass, grid = most < 1 ? 1 : most > 2048 ? 2048 : most;
     hipLaunchKernelGGL(chain_prepare, dim3((unsigned)grid), dim3(kNT), 0, st, static_cast<uint4 *>(q.workspace), count, q.cu,
                        q.B, q.T, q.D, from, to);
     const hipError_t e = hipGetLastError();

@@ -391,3 +391,37 @@ def test_more_sequences_than_workgroups():
     check(p, [(slice(cu[n], cu[n + 1]), n) for n in some], "preact", o, h_T, gr)
     empty = torch.tensor(lens == 0, device=DEV)
     assert torch.equal(h_T[empty], p["h0"][empty]) and torch.equal(gr["dh0"][empty], p["dhT"][empty])
+
+
+@pytest.mark.parametrize("N,T", [(4096, 64), (4096, 130), (4096, 0)])
+def test_states_of_empty_sequences_pass_through_by_the_whole_card(N, T):
+    """A few tokens among thousands of empty sequences: 64 MiB of states are passed on, in at most ten times a copy's
+    time and 100 us (one workgroup would take hundreds of times it), forward and backward."""
+    D = 4096
+    cu = torch.zeros(N + 1, dtype=torch.int32)
+    cu[N // 2:] = T  # all tokens in one sequence
+    cu = cu.to(DEV)
+    p = problem(np.random.default_rng(37), (max(T, 1),), D, 1, "channel", "f32")
+    x, a, b, dO = (p[k][:T] for k in ("x", "a", "b", "dO"))
+    h0 = torch.randn(N, D, device=DEV)
+    h_T = torch.empty_like(h0)
+
+    def us(f):
+        times = []
+        for _ in range(6):
+            s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            s.record()
+            f()
+            e.record()
+            e.synchronize()
+            times.append(s.elapsed_time(e) * 1e3)
+        return min(times[1:])
+
+    copy = us(lambda: h_T.copy_(h0))
+    fwd = us(lambda: g.linear_forward_varlen(x, a, b, cu, h0, h_T=h_T))
+    gr = {"dh0": torch.empty_like(h0)}
+    bwd = us(lambda: g.linear_backward_varlen(x, a, b, cu, h0, dO, h_T, grads=gr))
+    print(f"[linear empty sequences T {T}] copy {copy:.0f} us, forward {fwd:.0f}, backward {bwd:.0f}", flush=True)
+    rest = torch.arange(N, device=DEV) != (N // 2 - 1 if T else -1)
+    assert torch.equal(h_T[rest], h0[rest]) and torch.equal(gr["dh0"][rest], h_T[rest])
+    assert fwd <= 10 * copy + 100 and bwd <= 10 * copy + 100
