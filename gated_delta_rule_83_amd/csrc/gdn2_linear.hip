@@ -135,20 +135,23 @@ template <int VEC> struct Geo {
   static constexpr int PART = CT < 64 ? 64 : CT, WS = PART / CT, PARTS = kNT / PART;
 };
 
-// (A, U) := (a, u) after (A, U). CUT: a map with A = 0 takes nothing from what
-// lies before it, not even a NaN or an infinity: that is how a sequence of a
-// packed batch starts.
+// A map that takes nothing from what lies before it, not even a NaN or an
+// infinity: that is how a sequence of a packed batch starts. No product of
+// decays is this value; one that is 0 passes a NaN on.
+constexpr float kCut = -__builtin_huge_valf();
+
+// (A, U) := (a, u) after (A, U). CUT: either may be a cut.
 template <bool CUT> __device__ __forceinline__ void after(float a, float u, float &A, float &U) {
-  if (CUT && a == 0.f) {
-    A = 0.f;
+  if (CUT && a == kCut) {
+    A = kCut;
     U = u;
   } else {
     U = __builtin_fmaf(a, U, u);
-    A *= a;
+    A = CUT && A == kCut ? A : A * a;
   }
 }
 template <bool CUT> __device__ __forceinline__ float apply(float a, float u, float h) {
-  return CUT && a == 0.f ? u : __builtin_fmaf(a, h, u);
+  return CUT && a == kCut ? u : __builtin_fmaf(a, h, u);
 }
 
 // Where a tile's token tensors lie: the tile's first value, the bytes from a
@@ -279,14 +282,14 @@ __device__ __forceinline__ void take_tile(const Chain &ch, int *slot, int tid, i
 // first kLinChannels threads, from the tiles' published maps; own: this tile's
 // map. Publishes both. Every thread of the workgroup calls it. start: the value
 // entering the chain, in its first tile (0 in others). That tile publishes the
-// value leaving it as a map with A = 0, so that no other one reads where start
-// lies: the chain's last value may be written there.
+// value leaving it as a map that takes nothing, so that no other one reads where
+// start lies: the chain's last value may be written there.
 template <bool CUT>
 __device__ __forceinline__ float link(const Chain &ch, int k, int chain, float2 own, float start,
                                       float2 (*maps)[kLinChannels], int tid) {
   const int lane = tid % kLinChannels, w = tid / kLinChannels, in = k % kGroup;
   if (ch.tiles == 1) return start;
-  if (k == 0) own = float2{0.f, apply<CUT>(own.x, own.y, start)};
+  if (k == 0) own = float2{CUT ? kCut : 0.f, apply<CUT>(own.x, own.y, start)};
   if (w == 0 && in != kGroup - 1 && k != ch.tiles - 1)
     __hip_atomic_store(ch.map + ((size_t)k * ch.chains + chain) * kLinChannels + lane,
                        (uint64_t)word(own.x) | (uint64_t)word(own.y) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -467,14 +470,15 @@ __global__ __launch_bounds__(kNT, VEC == 4 ? 4 : 1) void linear_forward_chain(Li
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
           if (p.h0) u[i][c] = __builtin_fmaf(a[i][c], p.h0[(size_t)q * D + cc + c], u[i][c]);
-          A[c] = 0.f;
           U[c] = u[i][c];
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) after<false>(a[i][c], u[i][c], A[c], U[c]);
+        for (int c = 0; c < VEC; ++c) U[c] = __builtin_fmaf(a[i][c], U[c], u[i][c]);
       }
     }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) A[c] = kCut;
   }
   wave_scan<VEC, false, PACKED>(A, U, tot, tid);
   __syncthreads();
@@ -654,10 +658,14 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
         GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
         const float from = first ? (p.h0 ? p.h0[(size_t)edges[0].start[s * G::L + i] * D + cc + c] : 0.f) : U[c];
         U[c] = __builtin_fmaf(a, from, b * x[i][c]);
-        A[c] = first ? 0.f : A[c] * a;
+        A[c] *= a;
         Um[c] = am * (dr[j][c] + (cut ? last[s * G::L + j][ct * VEC + c] : Um[c]));
-        Am[c] = cut ? 0.f : Am[c] * am;
       }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      Am[c] = ends ? kCut : A[c];
+      A[c] = starts ? kCut : A[c];
     }
   }
   hold();

@@ -425,3 +425,32 @@ def test_states_of_empty_sequences_pass_through_by_the_whole_card(N, T):
     rest = torch.arange(N, device=DEV) != (N // 2 - 1 if T else -1)
     assert torch.equal(h_T[rest], h0[rest]) and torch.equal(gr["dh0"][rest], h_T[rest])
     assert fwd <= 10 * copy + 100 and bwd <= 10 * copy + 100
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("value", [0.05, 0.0])
+@pytest.mark.parametrize("D", [5, 64])
+def test_a_bad_token_reaches_its_sequences_end(D, value, packed):
+    """With decays whose product over a tile is 0 in fp32 (and with decays of 0: 0 * NaN is NaN) a NaN still reaches
+    every later token of its sequence, and in the backward every earlier one, but no other sequence."""
+    cu, n = [0, 30, 730, 900], 1
+    p = problem(np.random.default_rng(41), (900,), D, 3, "channel", "f32")
+    p["a"].fill_(value)
+    p["x"][100], p["dO"][650] = float("nan"), float("nan")
+    if packed:
+        cud = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        o, h_T, ck = g.linear_forward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], want_checkpoints=True)
+        gr = g.linear_backward_varlen(p["x"], p["a"], p["b"], cud, p["h0"], p["dO"], p["dhT"], ck=ck)
+    else:
+        q = {k: p[k][None, 30:730] for k in ("x", "a", "b", "dO")}
+        o, h_T, ck = g.linear_forward(q["x"], q["a"], q["b"], p["h0"][1:2], want_checkpoints=True)
+        gr = g.linear_backward(q["x"], q["a"], q["b"], p["h0"][1:2], q["dO"], p["dhT"][1:2], ck=ck)
+        o, gr, cu, n = o[0], {k: v[0] if k != "dh0" else v for k, v in gr.items()}, [0, 700], 0
+    torch.cuda.synchronize()
+    lo, hi, bad, badO = cu[n], cu[n + 1], cu[n] + 70, cu[n] + 620
+    assert torch.isnan(o[bad:hi]).all() and torch.isnan(h_T[n]).all() and torch.isfinite(o[lo:bad]).all()
+    assert torch.isnan(gr["dx"][lo:badO + 1]).all() and torch.isnan(gr["dh0"][n]).all()
+    assert torch.isfinite(gr["dx"][badO + 1:hi]).all() and torch.isnan(gr["da"][bad + 1:hi]).all()
+    if packed:
+        p = dict(p, x=p["x"].nan_to_num(0.0), dO=p["dO"].nan_to_num(0.0))
+        check(p, [(slice(cu[m], cu[m + 1]), m) for m in (0, 2)], "channel", o, h_T, gr)
