@@ -59,58 +59,38 @@ template <int FORM, bool EXACT> __device__ __forceinline__ void activate(float &
   }
 }
 
-// A sigmoid and its complement in one word: the smaller of the two, the
-// complement with its sign set. Both come back without a difference that
-// loses digits.
-__device__ __forceinline__ float pack_pair(float p, float q) { return p <= q ? p : -q; }
-__device__ __forceinline__ void unpack_pair(float v, float &p, float &q) {
-  const float o = 1.f - __builtin_fabsf(v);
-  p = v > 0.f ? v : o;
-  q = v > 0.f ? o : -v;
+// A sigmoid p = 1 / (1 + e^x) and its complement q in one word v: the smaller of
+// the two, e^-|x| / (1 + e^-|x|), with x's sign, so p where that is at most 1/2
+// and -q above. Both come back, and p q, without a difference that loses digits:
+// a gradient through a nearly closed or open gate keeps its relative accuracy.
+// (What is added is the smallest normal number: v is never 0, which has no side.)
+constexpr float kNoSlope = 0x1p-126f;
+template <bool EXACT> __device__ __forceinline__ float pack_pair(float x) {
+  const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * -1.44269504088896341f), d = 1.f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  if constexpr (EXACT) r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+  return __builtin_copysignf(__builtin_fmaf(e, r, kNoSlope), x);
 }
+__device__ __forceinline__ float pair_p(float v) { return v - __builtin_floorf(v); }
+__device__ __forceinline__ float pair_q(float v) { return __builtin_ceilf(v) - v; }
+__device__ __forceinline__ float pair_pq(float v) { return __builtin_fmaf(-v, v, __builtin_fabsf(v)); }
 
-// A token's gates as the backward keeps them, one word each. For the gradient
-// through an activation, p (1 - p), fp32 pre-activations keep both factors
-// exact to their last digits (pack_pair). With bf16 ones the word is 1 - a (or
-// b) and the other factor its difference from 1: p (1 - p) is off by at most
-// 2^-24, which a bf16 gradient shows only where p is within 2^-15 of 0 (a) or
-// of 1 (b); unpacking pairs made that kernel bound by its arithmetic
-// (B1 T65536 D2048: 15% slower).
+// A token's gates as the backward keeps them, one word each: fp32 gates
+// themselves, pre-activations' as pairs.
 template <int FORM, bool EXACT> struct Gates {
   static __device__ __forceinline__ void pack(float &a, float &b) {
     if constexpr (Form<FORM>::pre) {
-      const float q = low_sigmoid<EXACT>(-a);
-      a = EXACT ? pack_pair(low_sigmoid<EXACT>(a), q) : q;
-      if constexpr (!Form<FORM>::tied) {
-        const float p = low_sigmoid<EXACT>(-b);
-        b = EXACT ? pack_pair(p, low_sigmoid<EXACT>(b)) : p;
-      }
+      a = pack_pair<EXACT>(a);
+      if constexpr (!Form<FORM>::tied) b = pack_pair<EXACT>(-b);
     }
   }
-  // a, 1 - a, b, 1 - b (the complements in the pre-activation forms only)
-  static __device__ __forceinline__ void unpack(float va, float vb, float &a, float &na, float &b, float &nb) {
-    if constexpr (Form<FORM>::pre) {
-      if constexpr (EXACT) {
-        unpack_pair(va, a, na);
-      } else {
-        na = va;
-        a = 1.f - va;
-      }
-      if constexpr (Form<FORM>::tied) {
-        b = na;
-      } else if constexpr (EXACT) {
-        unpack_pair(vb, b, nb);
-      } else {
-        b = vb;
-        nb = 1.f - vb;
-      }
-    } else {
-      a = va;
-      b = Form<FORM>::tied ? 1.f - va : vb;
-    }
+  static __device__ __forceinline__ void unpack(float va, float vb, float &a, float &b) {
+    a = Form<FORM>::pre ? pair_p(va) : va;
+    if constexpr (Form<FORM>::tied) b = Form<FORM>::pre ? pair_q(va) : 1.f - va;
+    else b = Form<FORM>::pre ? pair_p(vb) : vb;
   }
   // va of a token that passes the state on (a = 1)
-  static __device__ __forceinline__ float none() { return Form<FORM>::pre ? -0.f : 1.f; }
+  static __device__ __forceinline__ float none() { return Form<FORM>::pre ? -kNoSlope : 1.f; }
 };
 
 struct Lin {
@@ -636,13 +616,15 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
       const int j = G::L - 1 - i;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
-        float a, b, am, x0, x1, x2;
-        GT::unpack(va[i][c], vb[i][c], a, x0, b, x1);
-        GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
+        float a, b, am, bm;
+        GT::unpack(va[i][c], vb[i][c], a, b);
+        GT::unpack(va[j][c], vb[j][c], am, bm);
         U[c] = __builtin_fmaf(a, U[c], b * x[i][c]);
         A[c] *= a;
         Um[c] = am * (dr[j][c] + Um[c]);
       }
+      // packed single values: unpacking that runs ahead spills (fp32, 16384 x 1001: 159 us)
+      if constexpr (PACKED && VEC == 1 && Form<FORM>::pre) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) Am[c] = A[c];
@@ -653,9 +635,9 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
       const bool first = starts >> i & 1, cut = ends >> j & 1;
 #pragma unroll
       for (int c = 0; c < VEC; ++c) {
-        float a, b, am, x0, x1, x2;
-        GT::unpack(va[i][c], vb[i][c], a, x0, b, x1);
-        GT::unpack(va[j][c], vb[j][c], am, x0, x1, x2);
+        float a, b, am, bm;
+        GT::unpack(va[i][c], vb[i][c], a, b);
+        GT::unpack(va[j][c], vb[j][c], am, bm);
         const float from = first ? (p.h0 ? p.h0[(size_t)edges[0].start[s * G::L + i] * D + cc + c] : 0.f) : U[c];
         U[c] = __builtin_fmaf(a, from, b * x[i][c]);
         A[c] *= a;
@@ -688,8 +670,8 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      float a, na, b, nb;
-      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
+      float a, b;
+      GT::unpack(va[i][c], vb[i][c], a, b);
       hp[i][c] = h[c];
       h[c] = __builtin_fmaf(a, h[c], b * x[i][c]);
     }
@@ -709,16 +691,16 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      float a, na, b, nb;
-      GT::unpack(va[i][c], vb[i][c], a, na, b, nb);
+      float a, b;
+      GT::unpack(va[i][c], vb[i][c], a, b);
       const float g = dr[i][c] + mi[c], xv = x[i][c];
       mi[c] = a * g;
       dx[c] = b * g;
       db[c] = xv * g;
       da[c] = Form<FORM>::tied ? g * (hp[i][c] - xv) : g * hp[i][c];
       if constexpr (Form<FORM>::pre) {  // through the activations: a' = -a (1 - a), b' = b (1 - b)
-        da[c] *= -a * na;
-        if constexpr (!Form<FORM>::tied) db[c] *= b * nb;
+        da[c] *= -pair_pq(va[i][c]);
+        if constexpr (!Form<FORM>::tied) db[c] *= pair_pq(vb[i][c]);
       }
     }
     if (own && (!ragged || t < p.T)) {

@@ -454,3 +454,43 @@ def test_a_bad_token_reaches_its_sequences_end(D, value, packed):
     if packed:
         p = dict(p, x=p["x"].nan_to_num(0.0), dO=p["dO"].nan_to_num(0.0))
         check(p, [(slice(cu[m], cu[m + 1]), m) for m in (0, 2)], "channel", o, h_T, gr)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", ["preact", "tied_preact"])
+@pytest.mark.parametrize("T,D,packed", [(1, 64, False), (1, 61, False), (128, 64, False), (128, 61, False), (128, 64, True)])
+def test_gradients_of_nearly_closed_and_open_gates(T, D, packed, form, dtype):
+    """Value by value: pre-activations of +-8 to +-20, where one of a gate and its complement is 2e-9 to 3e-4. States,
+    adjoints and terms are all of one sign, so nothing cancels and each gradient is held to its own size: T tokens'
+    30 roundings (20 of them the exponential's argument's) for each of the state and the adjoint, 60 of the two
+    factors, and the output's one."""
+    rng = np.random.default_rng(43)
+    mk = lambda v, d: torch.tensor(np.asarray(v, np.float32)).to(d).to(DEV)
+    dt, shape = R.TORCH[dtype], (1, T, D)
+    far = np.linspace(8.0, 20.0, D) * np.where(np.arange(D) % 2, 1.0, -1.0)
+    # tied: h - x must not cancel, so x changes its sign from token to token (a closed gate's h is the x before)
+    sign = np.where(np.arange(T) % 2, -1.0, 1.0)[None, :, None] if form == "tied_preact" else 1.0
+    x, dO = sign * rng.uniform(0.5, 1.5, shape), rng.uniform(0.5, 1.5, shape)
+    a = np.ascontiguousarray(np.broadcast_to(far, shape))
+    b = np.ascontiguousarray(np.broadcast_to(np.roll(far, D // 2), shape))
+    h0, dhT = np.full((1, D), -3.0 if form == "tied_preact" else 3.0), np.full((1, D), 2.0)
+    p = dict(x=mk(x, dt), a=mk(a, dt), b=None if form == "tied_preact" else mk(b, dt), h0=mk(h0, torch.float32),
+             dO=mk(dO, dt), dhT=mk(dhT, torch.float32))
+    if packed:
+        q = {k: None if p[k] is None else p[k][0] for k in ("x", "a", "b", "dO")}
+        cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+        gr = g.linear_backward_varlen(q["x"], q["a"], q["b"], cu, p["h0"], q["dO"], p["dhT"], gates=form)
+    else:
+        gr = g.linear_backward(p["x"], p["a"], p["b"], p["h0"], p["dO"], p["dhT"], gates=form)
+    torch.cuda.synchronize()
+    f = {k: R.f64(v) for k, v in p.items()}
+    one = lambda k: None if f[k] is None else f[k][0]
+    dx, da, db, dh0, _ = R.linear_grads(f["x"][0], f["a"][0], one("b"), f["h0"][0], f["dO"][0], f["dhT"][0], form)
+    rel = (60 * T + 60) * R.U32
+    for name, got, ref, r in (("da", gr["da"], da, rel), ("db", gr["db"], db, rel), ("dx", gr["dx"], dx, rel), ("dh0", gr["dh0"], dh0, rel)):
+        if ref is None:
+            continue
+        r = r + (0.0 if got.dtype == torch.float32 else R.half(got.dtype) * (1 + r))
+        worst = (np.abs(R.f64(got).reshape(ref.shape) - ref) / (r * np.abs(ref))).max()
+        print(f"[linear gates {form} {dtype} T {T} {name}] worst error over its bound {worst:.3f}", flush=True)
+        assert worst <= 1.0, name
