@@ -502,8 +502,8 @@ __global__ __launch_bounds__(kNT, VEC == 4 ? 4 : 1) void linear_forward_chain(Li
 // The gradients, tile by tile from the last one: the adjoint is chained, the
 // states come from the saved ones. Two waves a SIMD: fp32 with untied gates and
 // packed single values would take a few registers past the half of them (B4
-// T4096 D2048 fp32 pre-activations 250 us instead of 202, packed 16384 x 1001
-// bf16 pre-activations 152 instead of 103).
+// T4096 D2048 fp32 pre-activations 229 us instead of 196, packed 16384 x 1001
+// bf16 pre-activations 150 instead of 101).
 template <bool BF16, int FORM, int VEC, bool PACKED>
 __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch) {
   using G = Geo<VEC>;
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(kNT, 2) void linear_backward_chain(Lin p, Chain ch)
         A[c] *= a;
         Um[c] = am * (dr[j][c] + Um[c]);
       }
-      // packed single values: unpacking that runs ahead spills (fp32, 16384 x 1001: 159 us)
+      // packed single values: unpacking that runs ahead spills (fp32, 16384 x 1001: 159 us instead of 134)
       if constexpr (PACKED && VEC == 1 && Form<FORM>::pre) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll

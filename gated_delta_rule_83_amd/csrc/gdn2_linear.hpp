@@ -1,5 +1,5 @@
 // gdn2_linear.hpp -- launch interface of the gated linear recurrence
-// (gdn2_linear_api.cpp to gdn2_linear.hip). Not installed.
+// (gdn2_operators_api.cpp to gdn2_linear.hip). Not installed.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -49,7 +49,7 @@ gdn2_status check_linear(const gdn2_linear_desc *d, bool packed) {
   if (d->dtype != GDN2_F32 && d->dtype != GDN2_BF16) return GDN2_ERR_BAD_DTYPE;
   if (d->B < 0 || d->T < 0 || d->D < 1) return GDN2_ERR_BAD_SHAPE;
   if (d->gates < GDN2_LINEAR_CHANNEL || d->gates > GDN2_LINEAR_TIED_PREACT) return GDN2_ERR_UNSUPPORTED;
-  // a tile's 128 token rows are addressed with 32-bit offsets
+  // a tile's 64 token rows are addressed with 32-bit offsets
   if (d->T > INT32_MAX - 256 || d->D > 1 << 22) return GDN2_ERR_UNSUPPORTED;
   // workgroups: a tile of a chain each, and of whole sequences each has its own
   // chains; the products are below 2^25 * 2^15 and 2^24 * 2^31

@@ -607,8 +607,10 @@ typedef struct {
 } gdn2_cache_desc;
 
 /* Entry n's state into slot slots[n]. A slot outside [0, P) is skipped; of
- * entries that name the same slot the last one is kept. Slots that no entry
- * names are left as they were. */
+ * entries that name the same slot the last one is kept, for which each entry
+ * looks at all later ones: past some ten thousand entries of small states that
+ * grows with N^2 (d_v 16, rows 1: N 16384 47 us, 65536 0.5 ms, 262144 7.5 ms).
+ * Slots that no entry names are left as they were. */
 gdn2_status gdn2_state_cache_store(const gdn2_cache_desc *desc, const float *S, const int32_t *slots, void *cache,
                                    void *scales, void *stream);
 
