@@ -20,6 +20,11 @@ Next to the delta rule (raw gdn2_linear_*, gdn2_norm_*, gdn2_state_cache_* as we
     gated_linear_recurrence, gated_linear_recurrence_varlen (autograd)
     norm_forward(x, weight, bias, gate, eps, kind) -> y, norm_backward, norm (autograd)
     state_cache_empty, state_cache_store, state_cache_load          (states in 8 bits)
+Attention layers (raw gdn2_rotary_*, gdn2_attention_*, gdn2_kv_cache_store as well):
+    rotary_forward(q, k, positions, inv_freq, q_weight, k_weight, ...) -> (q, k), rotary_backward, rotary (autograd)
+    attention_forward(q, k, v, scale, causal, window) -> (o, lse), attention_forward_varlen, attention_backward,
+    attention_backward_varlen, attention, attention_varlen (autograd)
+    kv_cache_empty, kv_cache_store, attention_decode                (one token over a paged key-value cache)
 
 If ``libgdn2.so`` has not been built, loading fails loudly: there is no
 fallback path.
@@ -60,6 +65,11 @@ EXPORTED = ("gdn2_chunk_forward", "gdn2_chunk_forward_coupled", "gdn2_chunk_forw
             "gdn2_linear_backward_workspace_bytes", "gdn2_linear_backward_varlen",
             "gdn2_linear_backward_varlen_workspace_bytes", "gdn2_norm_forward", "gdn2_norm_backward",
             "gdn2_norm_backward_workspace_bytes", "gdn2_state_cache_store", "gdn2_state_cache_load",
+            "gdn2_rotary_forward", "gdn2_rotary_backward", "gdn2_rotary_backward_workspace_bytes",
+            "gdn2_attention_forward", "gdn2_attention_forward_varlen", "gdn2_attention_backward",
+            "gdn2_attention_backward_workspace_bytes", "gdn2_attention_backward_varlen",
+            "gdn2_attention_backward_varlen_workspace_bytes", "gdn2_attention_decode",
+            "gdn2_attention_decode_workspace_bytes", "gdn2_kv_cache_store",
             "gdn2_status_string", "gdn2_version")
 
 
@@ -126,7 +136,7 @@ def load(path: Optional[str] = None):
     lib.gdn2_chunk_backward_varlen.argtypes = [dp] + [vp] * 17 + [vp, sz, vp]
     lib.gdn2_chunk_backward_varlen_workspace_bytes.restype = sz
     lib.gdn2_chunk_backward_varlen_workspace_bytes.argtypes = [dp]
-    for part in (linear, norms, state_cache):
+    for part in (linear, norms, state_cache, rotary_ops, attention_ops):
         part.declare(lib)
     lib.gdn2_status_string.restype = ctypes.c_char_p
     lib.gdn2_status_string.argtypes = [ctypes.c_int]
@@ -829,3 +839,13 @@ from .norms import (NORM_KINDS, gdn2_norm_backward, gdn2_norm_backward_workspace
                     gdn2_norm_forward, norm, norm_backward, norm_forward)
 from .state_cache import (CACHE_FORMATS, gdn2_cache_desc, gdn2_state_cache_load, gdn2_state_cache_store,  # noqa: E402,F401
                           state_cache_empty, state_cache_load, state_cache_store)
+from . import attention_ops, rotary_ops  # noqa: E402
+from .rotary_ops import (PAIRS, gdn2_rotary_backward, gdn2_rotary_backward_workspace_bytes, gdn2_rotary_desc,  # noqa: E402,F401
+                     gdn2_rotary_forward, rotary, rotary_backward, rotary_forward)
+from .attention_ops import (attention, attention_backward, attention_backward_varlen, attention_decode,  # noqa: E402,F401
+                        attention_forward, attention_forward_varlen, attention_varlen, gdn2_attention_backward,
+                        gdn2_attention_backward_varlen, gdn2_attention_backward_varlen_workspace_bytes,
+                        gdn2_attention_backward_workspace_bytes, gdn2_attention_decode, gdn2_attention_decode_desc,
+                        gdn2_attention_decode_workspace_bytes, gdn2_attention_desc, gdn2_attention_forward,
+                        gdn2_attention_forward_varlen, gdn2_kv_cache_desc, gdn2_kv_cache_store, kv_cache_empty,
+                        kv_cache_store)

@@ -59,3 +59,41 @@ class launch_on:
         if self._ctx is not None:
             self._ctx.__exit__(*exc)
         return False
+
+
+def want_tokens(t, name, shape, dtype, device):
+    """t must be `shape` [..., heads, d] on `device` with every token's heads
+    contiguous and the tokens one distance apart; that distance in elements."""
+    if t.is_contiguous():
+        want(t, name, shape, dtype, device)
+        return t.shape[-2] * t.shape[-1]
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a torch tensor on a GPU")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, but q is on {device}")
+    *lead, H, d = t.shape
+    *steps, head, one = t.stride()
+    if t.numel() == 0:
+        return H * d
+    step = reach = None
+    for n, s in zip(reversed(lead), reversed(steps)):
+        if n == 1:
+            continue
+        if step is None:
+            step, reach = s, s * n
+        elif s != reach:
+            step = -1
+            break
+        else:
+            reach *= n
+    if step is None:
+        step = H * d
+    if (d > 1 and one != 1) or (H > 1 and head != d) or step < H * d:
+        raise ValueError(f"{name} must hold each token's [heads, d] contiguously and its tokens one distance apart, "
+                         f"got strides {t.stride()} for shape {tuple(t.shape)}")
+    return step

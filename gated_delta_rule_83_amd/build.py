@@ -34,6 +34,9 @@ def _units():
     units = [("gdn2_api.cpp", "api", []), ("gdn2_operators_api.cpp", "operators_api", []),
              ("gdn2_linear.hip", "linear", []), ("gdn2_norm.hip", "norm", []),
              ("gdn2_norm.hip", "norm_backward", ["-DGDN2_NORM_BACKWARD"]), ("gdn2_state_cache.hip", "state_cache", []),
+             ("gdn2_attention_api.cpp", "attention_api", []), ("gdn2_rotary.hip", "rotary", []),
+             ("gdn2_attention.hip", "attention", []), ("gdn2_attention_backward.hip", "attention_backward", []),
+             ("gdn2_attention_decode.hip", "attention_decode", []),
              ("gdn2_decode.hip", "decode", []),
              ("gdn2_prefill.hip", "prefill", []), ("gdn2_noalloc.hip", "noalloc", []),
              ("gdn2_backward_chunk.hip", "backward_chunk", [])]

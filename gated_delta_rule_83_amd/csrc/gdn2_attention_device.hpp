@@ -1,0 +1,360 @@
+// gdn2_attention_device.hpp -- tiles, operands and masks that the attention
+// kernels share (gfx950 only).
+//
+// Every product runs on 32 x 32 accumulators (lane l: column l & 31, half
+// h = l >> 5; register i: row 8 (i / 4) + 4 h + i % 4) over steps of 16 of the
+// contracted axis, whose operands hold 8 values a lane: row (A) or column (B)
+// l & 31, values 8 h .. 8 h + 7 of the step. Two facts carry the kernels:
+//  - an accumulator's registers 8 s .. 8 s + 7, read as rows of the contracted
+//    axis, are already a B operand if the A operand takes the same order:
+//    slot j is row 16 s + 8 (j / 4) + 4 h + j % 4. So scores become the next
+//    product's operand in registers.
+//  - a column of such an accumulator belongs to one lane (and its partner of
+//    the other half): scores are kept transposed where a softmax row has to
+//    be a column, so row statistics are sums over a lane's own registers.
+// bf16 operands of columns of a tile come from LDS with transposing reads, so
+// a tile lies there once, row by row.
+#pragma once
+
+#include "gdn2_attention.hpp"
+#include "gdn2_vec.hpp"
+
+namespace gdn2 {
+namespace attn {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx8 __attribute__((ext_vector_type(8)));
+typedef short shortx8 __attribute__((ext_vector_type(8)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+template <bool BF16> struct Frag;
+template <> struct Frag<true> { bf16x8 v; };
+template <> struct Frag<false> { floatx8 v; };
+
+template <bool BF16> __device__ __forceinline__ floatx16 mma(floatx16 acc, const Frag<BF16> &a, const Frag<BF16> &b) {
+  if constexpr (BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+  } else {
+    // one step of 2 takes value j of both halves: 8 of them are a step of 16 in the same order
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], acc, 0, 0, 0);
+    return acc;
+  }
+}
+
+__device__ __forceinline__ floatx16 zero16() {
+  floatx16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// registers 8 s .. 8 s + 7 of an accumulator as an operand
+template <bool BF16> __device__ __forceinline__ Frag<BF16> operand(const floatx16 &x, int s) {
+  floatx8 y;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = x[8 * s + j];
+  if constexpr (BF16) return Frag<true>{__builtin_convertvector(y, bf16x8)};
+  else return Frag<false>{y};
+}
+
+// row of register i of a lane of half h
+__device__ __forceinline__ constexpr int row_of(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// ---------------------------------------------------------------- tiles in LDS
+// R rows of D values, 16-byte chunks exchanged within a row so that neither 16
+// rows of one chunk nor 4 rows of 64 bytes meet in a bank.
+template <bool BF16, int D> struct Tile {
+  static constexpr int ES = BF16 ? 2 : 4, ROW = D * ES, CHUNKS = ROW / 16;
+  static __device__ __forceinline__ int swizzle(int r) {
+    if constexpr (CHUNKS >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+    else return ((r & 2) << 1) | ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swizzle(r)) << 4); }
+
+  // row r, values 16 kk + 8 h ..: an operand whose contracted axis runs along the rows
+  static __device__ __forceinline__ Frag<BF16> along(const char *t, int r, int kk, int h) {
+    if constexpr (BF16) {
+      return Frag<true>{*reinterpret_cast<const bf16x8 *>(t + at(r, 2 * kk + h))};
+    } else {
+      const floatx4 x = *reinterpret_cast<const floatx4 *>(t + at(r, 4 * kk + 2 * h));
+      const floatx4 y = *reinterpret_cast<const floatx4 *>(t + at(r, 4 * kk + 2 * h + 1));
+      return Frag<false>{__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)};
+    }
+  }
+
+  // column c0 + (lane & 31), slots j = rows r0 + 8 (j / 4) + 4 h + j % 4: an
+  // operand whose contracted axis runs across the rows. bf16: in a transposing
+  // read lane 4 a + b of 16 receives value b of the 8 bytes that lanes a, a + 4,
+  // a + 8 and a + 12 address, so lane j addresses row j / 4, columns 4 (j % 4).
+  static __device__ __forceinline__ Frag<BF16> across(const char *t, int r0, int c0, int lane) {
+    const int h = lane >> 5;
+    if constexpr (BF16) {
+      const int col = c0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), r = r0 + 4 * h + ((lane >> 2) & 3);
+      auto rd = [&](int row) {
+        const char *src = t + at(row, col >> 3) + 2 * (col & 7);
+        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4i16 *)(__attribute__((address_space(3))) const char *)src));
+      };
+      return Frag<true>{__builtin_shufflevector(rd(r), rd(r + 8), 0, 1, 2, 3, 4, 5, 6, 7)};
+    } else {
+      const int col = c0 + (lane & 31);
+      Frag<false> f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f.v[j] = *reinterpret_cast<const float *>(t + at(r0 + 8 * (j >> 2) + 4 * h + (j & 3), col >> 2) + 4 * (col & 3));
+      return f;
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
+// R rows straight from memory into a tile: 16 bytes a lane, which land in LDS
+// in the order of the lanes; the exchange of chunks is in the addresses read.
+// The wave-uniform part of an address is the buffer's base, so that a lane
+// keeps one offset for all tiles. Rows past the last one are outside the
+// buffer (zeros, or what the tile held); they are never visible. The compiler
+// does not see these loads: landed() before the barrier that hands a tile over.
+// 64 lanes' 16 (or 4) bytes at base + off, bounded by `bytes`, to LDS address `to` on.
+template <int BYTES> __device__ __forceinline__ void dma(const char *base, uint32_t bytes, uint32_t off, uint32_t to) {
+  const uintx4 rsrc = {uniform((uint32_t)(uintptr_t)base), uniform((uint32_t)((uintptr_t)base >> 32)) & 0xffffu, uniform(bytes),
+                       0x00020000u};
+  // nothing else in these kernels uses m0; the nop is the wait between its write and its use
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(uniform(to)), "v"(off), "s"(rsrc)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(uniform(to)), "v"(off), "s"(rsrc)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)static_cast<const char *>(p);
+}
+
+template <bool BF16, int D, int R, int THREADS = 256> struct Dma {
+  using L = Tile<BF16, D>;
+  static constexpr int N = R * L::CHUNKS / THREADS, RPI = THREADS / L::CHUNKS;  // rows of one turn
+  static_assert(R * L::CHUNKS % THREADS == 0 && THREADS % L::CHUNKS == 0, "whole rows a turn");
+  static constexpr int OFFS = RPI % 16 ? 16 / RPI : 1;  // turns after which the exchange repeats
+  uint32_t off[OFFS], stride;
+  // s: bytes between rows
+  __device__ __forceinline__ void init(int64_t s, int tid) {
+    stride = (uint32_t)s;
+#pragma unroll
+    for (int i = 0; i < OFFS; ++i) {
+      const int r = tid / L::CHUNKS + i * RPI;
+      off[i] = (tid / L::CHUNKS) * stride + (((tid % L::CHUNKS) ^ L::swizzle(r)) << 4);
+    }
+  }
+  // base: row 0 of the sequence and head
+  __device__ __forceinline__ void load(const char *tile, const char *base, int row0, int n, int wave) const {
+    const uint32_t rows = (uint32_t)min(n - row0, R), to = lds_address(tile) + wave * 1024;
+    const char *from = base + (int64_t)row0 * stride;
+    // the whole offset in the lane's part: the bounds check does not hold for a uniform part past the end
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      dma<16>(from, (rows - 1) * stride + L::ROW, off[i % OFFS] + i * RPI * stride, to + i * THREADS * 16);
+  }
+};
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Row `row` of a tensor as B operands of the steps along it (values 16 kk + 8 h ..).
+template <bool BF16, int D> __device__ __forceinline__ void load_row(Frag<BF16> (&f)[D / 16], const char *row, int h) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    if constexpr (BF16) {
+      f[kk].v = *reinterpret_cast<const bf16x8 *>(row + (16 * kk + 8 * h) * 2);
+    } else {
+      const floatx4 *p = reinterpret_cast<const floatx4 *>(row + (16 * kk + 8 * h) * 4);
+      f[kk].v = __builtin_shufflevector(p[0], p[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+}
+
+// An accumulator of D / 32 blocks whose column is a row of the tensor at `row`, times f.
+template <bool BF16, int D> __device__ __forceinline__ void store_row(char *row, const floatx16 (&acc)[D / 32], float f, int h) {
+#pragma unroll
+  for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float x[4] = {acc[b][i] * f, acc[b][i + 1] * f, acc[b][i + 2] * f, acc[b][i + 3] * f};
+      store_at<BF16, 4>(row + (32 * b + row_of(i, h)) * (BF16 ? 2 : 4), x);
+    }
+}
+
+// ---------------------------------------------------------------- values in hidden places
+// In a tile of which some places are hidden, an infinity or NaN there must leave
+// nothing, though 0 times it is NaN, and one in a place that a row sees must
+// make that row's result NaN in its column. So the workgroup looks through such
+// a tile first; where it holds one (rare), it is replaced by zero and noted, a
+// byte for 16 bytes of the tile, and poison() puts NaN into the results that
+// see it.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {  // sign bits of the bf16 halves that are no number
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ bool odd(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
+
+// Notes of one tile, and a word of each wave.
+template <bool BF16, int D, int R> struct Odd {
+  uint8_t note[R * Tile<BF16, D>::CHUNKS];
+  uint32_t wave[4];
+};
+
+// The whole workgroup (256 threads) calls; true: the tile held some, and `o` says where.
+template <bool BF16, int D, int R> __device__ __forceinline__ bool clean(char *t, Odd<BF16, D, R> &o, int tid) {
+  constexpr int N = R * Tile<BF16, D>::CHUNKS;
+  bool f = false;
+#pragma unroll
+  for (int i = 0; i < N / 256; ++i) {
+    const uintx4 w = *reinterpret_cast<const uintx4 *>(t + (tid + i * 256) * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f |= BF16 ? odd_halves(w[j]) != 0 : odd(w[j]);
+  }
+  const bool any = __any(f);
+  if ((tid & 63) == 0) o.wave[tid >> 6] = any;
+  __syncthreads();
+  if (!uniform(o.wave[0] | o.wave[1] | o.wave[2] | o.wave[3])) return false;
+#pragma unroll 1
+  for (int i = tid; i < N; i += 256) {
+    uintx4 w = *reinterpret_cast<const uintx4 *>(t + i * 16);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        const uint32_t m = odd_halves(w[j]);
+        bits |= ((m >> 15) & 1u) << (2 * j) | (m >> 31) << (2 * j + 1);
+        w[j] &= ~((m >> 15) * 0xffffu);
+      } else if (odd(w[j])) {
+        bits |= 1u << j;
+        w[j] = 0;
+      }
+    }
+    o.note[i] = (uint8_t)bits;
+    *reinterpret_cast<uintx4 *>(t + i * 16) = w;
+  }
+  __syncthreads();
+  return true;
+}
+
+// Rows first .. last of the tile are those this lane's column sees.
+template <bool BF16, int D, int R>
+__device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const Odd<BF16, D, R> &o, int first, int last, int h) {
+  first = max(first, 0);
+  last = min(last, R - 1);
+#pragma unroll 1
+  for (int r = first; r <= last; ++r)
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int col = 32 * b + row_of(i, h);
+        const uint32_t bits = BF16 ? o.note[Tile<BF16, D>::at(r, col >> 3) >> 4] >> (col & 4) : o.note[Tile<BF16, D>::at(r, col >> 2) >> 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((bits >> e) & 1u) acc[b][i + e] = __builtin_nanf("");
+      }
+}
+
+// ---------------------------------------------------------------- sequences and blocks
+// Query i of n_q sees key j of n_k if lo(i) <= j <= hi(i), its own place on the
+// key axis being i + n_k - n_q.
+struct Mask {
+  int nq, nk, shift, window;
+  bool causal;
+  __device__ __forceinline__ int hi(int i) const { return causal ? min(i + shift, nk - 1) : nk - 1; }
+  __device__ __forceinline__ int lo(int i) const {
+    return window ? (int)max((int64_t)i + shift - window + 1, (int64_t)0) : 0;
+  }
+  // the queries that see key j: first .. last
+  __device__ __forceinline__ int first(int j) const { return causal ? (int)max((int64_t)j - shift, (int64_t)0) : 0; }
+  __device__ __forceinline__ int last(int j) const {
+    return window ? (int)min((int64_t)j - shift + window - 1, (int64_t)nq - 1) : nq - 1;
+  }
+};
+
+__device__ __forceinline__ int clamp_to(int x, int T) { return x < 0 ? 0 : (x > T ? T : x); }
+
+// Packed sequences: block slots s of sequence n are cu[n] / 128 + n .. , which
+// leaves every sequence room for its ragged last block; the workgroup finds n
+// by 64 tries at once.
+__device__ __forceinline__ bool find_block(const int32_t *cu, int B, int T, int s, int *seq, int *row0) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, cnt = B;
+  while (cnt > 1) {
+    const int step = (cnt + 63) >> 6, i = lane * step;
+    const bool below = i < cnt && clamp_to(cu[lo + min(i, cnt - 1)], T) / 128 + lo + i <= s;
+    const uint64_t b = __ballot(below);
+    const int c = b ? 63 - __builtin_clzll(b) : 0;
+    lo = __builtin_amdgcn_readfirstlane(lo + c * step);
+    cnt = min(step, cnt - c * step);
+    cnt = __builtin_amdgcn_readfirstlane(cnt);
+  }
+  *seq = lo;
+  *row0 = (s - (clamp_to(cu[lo], T) / 128 + lo)) * 128;
+  return *row0 >= 0;
+}
+
+// Neighbouring workgroups go to the 8 dies in turn; work w = (head, block) runs
+// so that each die takes a contiguous piece, whose heads share keys in its L2.
+// Blocks of a head run longest and shortest in turn, so that pieces are even.
+__device__ __forceinline__ bool find_work(unsigned total, unsigned tiles, unsigned *head, unsigned *tile) {
+  const unsigned per = (total + 7) >> 3, w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || w >= total) return false;
+  *head = w / tiles;
+  const unsigned t = w % tiles;
+  *tile = t & 1 ? t >> 1 : tiles - 1 - (t >> 1);
+  return true;
+}
+
+// A sequence's tokens: the first query and key over the whole batch, how many there are, and
+// the first of `head`'s values of a [head, query] array (lse, delta).
+struct Span {
+  int64_t q0, k0, rows;
+  Mask m;
+};
+// unit: b * heads + head (batch) or head (packed, sequence seq)
+__device__ __forceinline__ Span span_of(const AttentionArgs &p, int seq, int head) {
+  Span s;
+  s.m.causal = p.causal;
+  s.m.window = p.window;
+  if (p.cu_q) {
+    const int a = clamp_to(p.cu_q[seq], p.Tq), b = clamp_to(p.cu_q[seq + 1], p.Tq);
+    const int c = clamp_to(p.cu_k[seq], p.Tk), d = clamp_to(p.cu_k[seq + 1], p.Tk);
+    s.m.nq = max(b - a, 0);
+    s.m.nk = max(d - c, 0);
+    s.q0 = a;
+    s.k0 = c;
+    s.rows = (int64_t)head * p.Tq + a;
+  } else {
+    s.m.nq = p.Tq;
+    s.m.nk = p.Tk;
+    s.q0 = (int64_t)seq * p.Tq;
+    s.k0 = (int64_t)seq * p.Tk;
+    s.rows = ((int64_t)seq * p.H + head) * p.Tq;
+  }
+  s.m.shift = s.m.nk - s.m.nq;
+  return s;
+}
+
+// x combined with the other half's lane
+__device__ __forceinline__ float other_half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float other_half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+}  // namespace attn
+}  // namespace gdn2

@@ -14,33 +14,19 @@
 
 using gdn2::aligned16;
 using gdn2::aligned4;
+using gdn2::aligned_to;
+using gdn2::ceil_div;
+using gdn2::kMaxGroups;
 using gdn2::overlaps;
 using gdn2::Range;
 using gdn2::range_of;
 
 namespace {
 
-constexpr size_t kMaxGroups = (1u << 24) - 1;  // workgroups of 256 threads of one launch
-
-size_t ceil_div(size_t x, size_t y) { return (x + y - 1) / y; }
-
-// Whether p is aligned to its elements of `bytes` bytes.
-bool aligned_to(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
 gdn2_status status_of(hipError_t e) { return e == hipSuccess ? GDN2_OK : GDN2_ERR_HIP; }
 
-// Outputs against inputs and against each other; out[i] may be in[same[i]]
-// exactly (-1: none).
 gdn2_status check_overlap(const Range *in, int ni, const Range *out, int no, const int *same) {
-  for (int i = 0; i < no; ++i) {
-    for (int j = 0; j < ni; ++j) {
-      if (same[i] == j && out[i].lo == in[j].lo) continue;
-      if (overlaps(out[i], in[j])) return GDN2_ERR_ALIAS;
-    }
-    for (int j = i + 1; j < no; ++j)
-      if (overlaps(out[i], out[j])) return GDN2_ERR_ALIAS;
-  }
-  return GDN2_OK;
+  return gdn2::outputs_overlap(in, ni, out, no, same) ? GDN2_ERR_ALIAS : GDN2_OK;
 }
 
 // ------------------------------------------------------------------ linear recurrence

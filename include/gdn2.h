@@ -619,6 +619,168 @@ gdn2_status gdn2_state_cache_store(const gdn2_cache_desc *desc, const float *S, 
 gdn2_status gdn2_state_cache_load(const gdn2_cache_desc *desc, const void *cache, const void *scales,
                                   const int32_t *slots, float *S, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention layers, as hybrid models stack them between layers of the delta
+ * rule: queries and keys normed by head and rotated by position
+ * (gdn2_rotary_*), softmax attention over whole and packed sequences with its
+ * gradients (gdn2_attention_*), and for serving a paged cache of keys and
+ * values (gdn2_kv_cache_store) with the attention of one new token over it
+ * (gdn2_attention_decode). The conventions above hold; what differs is said.
+ *
+ * Tokens of q, k and v may lie apart: stride_* is the distance of two tokens in
+ * elements (0: one behind the other, heads * d), so that parts of one fused
+ * projection are taken as they are. A token's heads are contiguous; every
+ * other tensor is contiguous altogether. */
+
+/* Which values of a head turn together: value p with value p + rot / 2, or
+ * values 2 p and 2 p + 1 (p < rot / 2). Values from rot on are not turned. */
+typedef enum { GDN2_PAIRS_HALVES = 0, GDN2_PAIRS_NEIGHBOURS = 1 } gdn2_pairs;
+
+/* Norm of each head and rotation by position, queries and keys at once:
+ *
+ *   u = x / sqrt(mean(x^2) + eps) * weight         (norm != 0; else u = x * weight)
+ *   (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin)
+ *
+ * for each pair p, the angle being positions[token] * inv_freq[p], a product
+ * that is not rounded before it is brought within one turn: any position is as
+ * exact as position 1.
+ *   q, q_out : [tokens, H_q, d]    k, k_out : [tokens, H_k, d]   in dtype
+ *   q_weight, k_weight : [d] in wdtype, or NULL (ones)
+ *   positions : [tokens] int32     inv_freq : [rot / 2] fp32
+ * d even, 2 to 1024; rot even, 0 to d; H_q or H_k may be 0 (its tensors unused);
+ * H * d and strides up to 2^22, tokens up to 2^31 - 1 (GDN2_ERR_UNSUPPORTED past them). Tensors need only
+ * be aligned to their elements; where d <= 256 and rot are multiples of 8, and
+ * tensors (and strides) of 4 elements, rows are moved with wide loads. Arithmetic
+ * is fp32 with one rounding of each output. Outputs may not overlap inputs. */
+typedef struct {
+  int64_t tokens;
+  int32_t H_q, H_k, d, rot;
+  int32_t norm;   /* 0 or 1 */
+  int32_t pairs;  /* a gdn2_pairs */
+  int32_t dtype;  /* a gdn2_dtype: q, k, their results and gradients */
+  int32_t wdtype; /* a gdn2_dtype: the weights and their gradients */
+  float eps;
+  int64_t stride_q, stride_k;
+} gdn2_rotary_desc;
+
+gdn2_status gdn2_rotary_forward(const gdn2_rotary_desc *desc, const void *q, const void *k, const void *q_weight,
+                                const void *k_weight, const int32_t *positions, const float *inv_freq, void *q_out,
+                                void *k_out, void *stream);
+
+/* Gradients of gdn2_rotary_forward from its inputs and dq_out, dk_out (the
+ * shapes of q_out and k_out).
+ *   dq, dk : like q_out, k_out.
+ *   dq_weight, dk_weight : [d] in wdtype, summed over tokens and heads in fp32
+ *       and in a fixed order, or NULL (required NULL without the weight). No
+ *       tokens, or no heads at all, give zeros.
+ * workspace: gdn2_rotary_backward_workspace_bytes(desc) bytes, 16-byte aligned
+ * (not used where no weight's gradient is wanted). */
+size_t gdn2_rotary_backward_workspace_bytes(const gdn2_rotary_desc *desc);
+gdn2_status gdn2_rotary_backward(const gdn2_rotary_desc *desc, const void *q, const void *k, const void *q_weight,
+                                 const void *k_weight, const int32_t *positions, const float *inv_freq,
+                                 const void *dq_out, const void *dk_out, void *dq, void *dk, void *dq_weight,
+                                 void *dk_weight, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Softmax attention with grouped heads (query head h reads key head
+ * h / (H / H_kv)):
+ *
+ *   o_i = sum_j exp(s_ij - lse_i) v_j,   s_ij = scale q_i . k_j,
+ *   lse_i = log sum_j exp(s_ij)          over the keys j that query i sees
+ *
+ * Query i of T_q stands at place i + T_k - T_q of the key axis (queries are the
+ * last tokens of their keys, so keys may hold a prefix). It sees all keys, or
+ * (causal) those up to its place, or (window > 0, causal only) the last `window`
+ * of those. A query that sees no key gives o = 0 and lse = -inf, and no gradient.
+ *   q : [B, T_q, H, d]   k, v : [B, T_k, H_kv, d]   o : [B, T_q, H, d]   in dtype
+ *   lse : [B, H, T_q] fp32, may be NULL in the forward
+ * d 64 or 128 (GDN2_ERR_UNSUPPORTED otherwise); scale > 0, finite; any B, T >= 0 with
+ * B * H * ceil(T / 128) <= 2^24 - 1 (both T), T <= 2^31 - 257; H * d and strides up to 2^22.
+ * Tensors and strides are 16-byte aligned, lse and offsets 4-byte.
+ * Scores, sums and softmax are fp32; with bf16 inputs the probabilities (and
+ * their gradients) are rounded to bf16 once as operands of the matrix products,
+ * and every output once. NaN and infinities reach exactly the results that see them. */
+typedef struct {
+  int32_t B, T_q, T_k, H, H_kv, d;
+  int32_t causal; /* 0 or 1 */
+  int32_t window; /* 0: none */
+  int32_t dtype;  /* a gdn2_dtype */
+  float scale;
+  int64_t stride_q, stride_k, stride_v;
+} gdn2_attention_desc;
+
+gdn2_status gdn2_attention_forward(const gdn2_attention_desc *desc, const void *q, const void *k, const void *v,
+                                   void *o, float *lse, void *stream);
+
+/* B sequences packed along the token axes: q, o are [T_q, H, d], k, v
+ * [T_k, H_kv, d], lse [H, T_q]; sequence n's queries are tokens cu_q[n] ..
+ * cu_q[n+1]-1 and its keys cu_k[n] .. cu_k[n+1]-1 (B + 1 non-decreasing int32
+ * device offsets each, clamped to the tokens there are; cu_k may be cu_q). Rows
+ * of o and lse outside every sequence are left as they were. The limits count
+ * T / 128 + B blocks. */
+gdn2_status gdn2_attention_forward_varlen(const gdn2_attention_desc *desc, const int32_t *cu_q, const int32_t *cu_k,
+                                          const void *q, const void *k, const void *v, void *o, float *lse,
+                                          void *stream);
+
+/* Gradients of the forward calls, from their inputs, o and lse, given dO (like
+ * o): dq like o, dk and dv [B, T_k, H_kv, d] (the sums over the query heads that
+ * share a key head). workspace: ..._workspace_bytes(desc) bytes, 16-byte aligned.
+ * Packed gradient rows outside every sequence are zero. Results are
+ * deterministic (no atomics). */
+size_t gdn2_attention_backward_workspace_bytes(const gdn2_attention_desc *desc);
+gdn2_status gdn2_attention_backward(const gdn2_attention_desc *desc, const void *q, const void *k, const void *v,
+                                    const void *o, const float *lse, const void *dO, void *dq, void *dk, void *dv,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn2_attention_backward_varlen_workspace_bytes(const gdn2_attention_desc *desc);
+gdn2_status gdn2_attention_backward_varlen(const gdn2_attention_desc *desc, const int32_t *cu_q, const int32_t *cu_k,
+                                           const void *q, const void *k, const void *v, const void *o,
+                                           const float *lse, const void *dO, void *dq, void *dk, void *dv,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* A paged key-value cache: k_cache, v_cache [P, H_kv, page, d] in dtype, `page`
+ * tokens a page (a power of two); pages [N, M] int32 is a table of N sequences'
+ * pages, lengths [N] int32 their tokens (clamped to [0, M * page]): token t of
+ * sequence n is row t % page of page pages[n][t / page]. M * page <= 2^30.
+ *
+ * Decode: one new token a sequence, the last of its lengths[n] tokens (already
+ * in the cache), sees all of them or (window > 0) the last `window`. Tokens of a
+ * page outside [0, P) are not seen; whatever a page holds behind a sequence's last
+ * token is not read into any result. A query that sees no token (or scores of -inf alone) gives zeros.
+ *   q, o : [N, H, d]    d 64 or 128; H % H_kv == 0; N * H and the call's workgroups up to 2^24 - 1
+ * The work is split over the longest length that the table has room for; the
+ * spans' partial results (fp32) lie in the workspace
+ * (gdn2_attention_decode_workspace_bytes(desc) bytes, 16-byte aligned). */
+typedef struct {
+  int32_t N, H, H_kv, d;
+  int32_t P, page, M;
+  int32_t window; /* 0: none */
+  int32_t dtype;  /* a gdn2_dtype */
+  float scale;
+} gdn2_attention_decode_desc;
+
+size_t gdn2_attention_decode_workspace_bytes(const gdn2_attention_decode_desc *desc);
+gdn2_status gdn2_attention_decode(const gdn2_attention_decode_desc *desc, const void *q, const void *k_cache,
+                                  const void *v_cache, const int32_t *pages, const int32_t *lengths, void *o,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* New tokens' keys and values into the cache. cu_seqlens (N + 1 non-decreasing
+ * int32 device offsets into T packed tokens) or NULL (T = N, one token a
+ * sequence); lengths[n] counts the sequence's tokens with the new ones, which are
+ * its last. k, v : [T, H_kv, d]. Tokens of no sequence, before a sequence's
+ * token 0, past the table, or of a page outside [0, P) are skipped; the rest of
+ * the cache is left as it was. Precondition: no two tokens of a call have the
+ * same place (sequences may share the pages that neither writes); where two do,
+ * that place holds parts of either. */
+typedef struct {
+  int32_t N, T, H_kv, d;
+  int32_t P, page, M;
+  int32_t dtype; /* a gdn2_dtype */
+  int64_t stride_k, stride_v;
+} gdn2_kv_cache_desc;
+
+gdn2_status gdn2_kv_cache_store(const gdn2_kv_cache_desc *desc, const int32_t *cu_seqlens, const void *k,
+                                const void *v, const int32_t *pages, const int32_t *lengths, void *k_cache,
+                                void *v_cache, void *stream);
+
 /* Static, human-readable text for a status code. */
 const char *gdn2_status_string(gdn2_status status);
 
