@@ -26,7 +26,7 @@ template <bool BF16, int D> struct Forward {
 };
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256, 2) attention_forward_kernel(const AttentionArgs p, unsigned total, unsigned tiles) {
+__global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forward_kernel(const AttentionArgs p, unsigned total, unsigned tiles) {
   using C = Forward<BF16, D>;
   using L = typename C::L;
   constexpr int KT = C::KT, SUB = KT / 32, ES = BF16 ? 2 : 4;
@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(256, 2) attention_forward_kernel(const Attenti
   const int wlast = min(wrow + 31, m.nq - 1);  // < wrow: a wave without queries
   Frag<BF16> q[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
+  arrived(q);
   const float c = p.scale * kLog2e;
   const int hi = m.hi(row), lo = m.lo(row);
   // tiles that some query of the workgroup, and of the wave, sees; keys that
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(256, 2) attention_forward_kernel(const Attenti
   float top = neg_inf(), sum = 0.f;
 
   // One tile's products. masked (uniform): some query does not see some key.
-  auto step = [&](const char *kt, const char *vt, int key0, bool masked) {
+  auto step = [&](const char *kt, const char *vt, int key0, bool masked) __attribute__((always_inline)) {
     floatx16 s[SUB];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) s[u] = zero16();
@@ -131,20 +132,26 @@ __global__ void __launch_bounds__(256, 2) attention_forward_kernel(const Attenti
     Dma<BF16, D, KT> ks, vs;
     ks.init(p.sk * ES, tid);
     vs.init(p.sv * ES, tid);
-    ks.load(sm.tile[t_lo & 1][0], kbase, t_lo * KT, m.nk, wave);
-    vs.load(sm.tile[t_lo & 1][1], vbase, t_lo * KT, m.nk, wave);
-    for (int t = t_lo; t < t_hi; ++t) {
+    ks.load(sm.tile[0][0], kbase, t_lo * KT, m.nk, wave);
+    vs.load(sm.tile[0][1], vbase, t_lo * KT, m.nk, wave);
+    // BUF: the tile's buffer, a constant, so that LDS addresses are a lane's own and an offset
+    auto turn = [&](int t, auto buf) __attribute__((always_inline)) {
+      constexpr int BUF = decltype(buf)::value;
       const int key0 = t * KT;
       landed();
       __syncthreads();  // tile t is there, and nobody reads tile t - 1 any more
       if (t + 1 < t_hi) {
-        ks.load(sm.tile[(t + 1) & 1][0], kbase, key0 + KT, m.nk, wave);
-        vs.load(sm.tile[(t + 1) & 1][1], vbase, key0 + KT, m.nk, wave);
+        ks.load(sm.tile[BUF ^ 1][0], kbase, key0 + KT, m.nk, wave);
+        vs.load(sm.tile[BUF ^ 1][1], vbase, key0 + KT, m.nk, wave);
       }
-      char *kt = sm.tile[t & 1][0], *vt = sm.tile[t & 1][1];
+      char *kt = sm.tile[BUF][0], *vt = sm.tile[BUF][1];
       const bool bad = (key0 < b_lo || key0 + KT - 1 > b_hi) && clean<BF16, D, KT>(vt, sm.notes, tid);
       if (key0 <= w_hi && key0 + KT > w_lo) step(kt, vt, key0, key0 < all_lo || key0 + KT - 1 > all_hi);
       if (bad) poison<BF16, D, KT>(acc, sm.notes, lo - key0, hi - key0, h);
+    };
+    for (int t = t_lo; t < t_hi; t += 2) {
+      turn(t, std::integral_constant<int, 0>{});
+      if (t + 1 < t_hi) turn(t + 1, std::integral_constant<int, 1>{});
     }
   }
 

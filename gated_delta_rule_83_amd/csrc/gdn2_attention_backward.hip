@@ -62,7 +62,11 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) attention_dq_kernel(const A
       for (int j = 0; j < 8; ++j) delta = __builtin_fmaf((float)o[kk].v[j], (float)g[kk].v[j], delta);
     delta = other_half_sum(delta);
   }
-  const float c = p.scale * kLog2e, lse = p.lse_in[sp.rows + row] * kLog2e;
+  arrived(q);
+  arrived(g);
+  float lse = p.lse_in[sp.rows + row] * kLog2e;
+  pin_regs(lse);
+  const float c = p.scale * kLog2e;
   if (mine < m.nq && h == 0) {
     p.delta[sp.rows + mine] = delta;
     p.lse[sp.rows + mine] = lse;
@@ -166,6 +170,8 @@ __global__ void __launch_bounds__(256, 1) attention_dkv_kernel(const AttentionAr
   Frag<BF16> k[D / 16], v[D / 16];
   load_row<BF16, D>(k, static_cast<const char *>(p.k) + ((sp.k0 + row) * p.sk + (int64_t)kv * D) * ES, h);
   load_row<BF16, D>(v, static_cast<const char *>(p.v) + ((sp.k0 + row) * p.sv + (int64_t)kv * D) * ES, h);
+  arrived(k);
+  arrived(v);
   const float c = p.scale * kLog2e;
   const int first = m.first(row), last = m.last(row);
   // query tiles that some key of the workgroup, and of the wave, is seen from;

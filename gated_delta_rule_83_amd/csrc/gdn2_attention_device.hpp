@@ -181,6 +181,13 @@ template <bool BF16, int D> __device__ __forceinline__ void load_row(Frag<BF16> 
   }
 }
 
+// The rows are there from here on. Left to itself the compiler waits for them where they are used first, inside
+// the loop, and with them for the tile that is on its way.
+template <class F, int N> __device__ __forceinline__ void arrived(F (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) pin_regs(f[i]);
+}
+
 // An accumulator of D / 32 blocks whose column is a row of the tensor at `row`, times f.
 template <bool BF16, int D> __device__ __forceinline__ void store_row(char *row, const floatx16 (&acc)[D / 32], float f, int h) {
 #pragma unroll
