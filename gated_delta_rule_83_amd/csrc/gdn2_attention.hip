@@ -1,11 +1,11 @@
 // gdn2_attention.hip -- softmax attention over whole sequences, forward.
 //
 // o_i = sum_j p_ij v_j, p_ij = exp(s_ij - lse_i), s_ij = scale q_i . k_j over
-// the keys j that query i sees. A workgroup takes 128 queries of one head, a
-// wave 32 of them, and walks the keys in tiles that LDS holds twice, the next
-// one on its way from memory. Scores are computed transposed (keys as
-// rows), so that a query's softmax is a sum over its lane's registers and the
-// probabilities are the next product's operand where they lie.
+// the keys j that query i sees. A workgroup takes 128 queries of one head and
+// walks the keys in tiles that LDS holds twice, the next one on its way from
+// memory. Scores are computed transposed (keys as rows), so that a query's
+// softmax is a sum over its lane's registers and the probabilities are the next
+// product's operand where they lie.
 #include "gdn2_attention_device.hpp"
 
 namespace gdn2 {
@@ -19,32 +19,27 @@ using namespace attn;
 // left out for nearly every tile.
 constexpr float kSlack = 8.f;
 
-template <bool BF16, int D> struct Forward {
-  static constexpr int KT = BF16 ? 64 : 32;  // keys of a tile: 16 KB of each of K and V at D = 128
-  using L = Tile<BF16, D>;
-  static constexpr int TILE = KT * L::ROW;
-};
-
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forward_kernel(const AttentionArgs p, unsigned total, unsigned tiles) {
-  using C = Forward<BF16, D>;
-  using L = typename C::L;
-  constexpr int KT = C::KT, SUB = KT / 32, ES = BF16 ? 2 : 4;
+__global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forward_kernel(const AttentionArgs p, unsigned units) {
+  using L = Tile<BF16, D>;
+  constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4;  // 16 KB a tile of K or V at D = 128
+  constexpr int TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
-    char tile[2][2][C::TILE];  // first: within the 64 KB that m0 addresses
-    Odd<BF16, D, KT> notes;
+    char tile[2][2][TILE];  // first: within the 64 KB that m0 addresses
+    uint32_t said[4];
   } sm;
-  unsigned unit, tile;
-  if (!find_work(total, tiles, &unit, &tile)) return;
+  unsigned unit, rank;
+  find_work(units, &unit, &rank);
+  const int tile = (int)(gridDim.x / units - 1 - rank);  // causal: the last block sees most
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block(p.cu_q, p.B, p.Tq, (int)tile, &seq, &row0)) return;
+    if (!find_block(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
     head = (int)(unit % (unsigned)p.H);
-    row0 = (int)tile * kAttnRows;
+    row0 = tile * kAttnRows;
   }
   const Span sp = span_of(p, seq, head);
   const Mask m = sp.m;
@@ -53,36 +48,39 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   const char *kbase = static_cast<const char *>(p.k) + (sp.k0 * p.sk + (int64_t)kv * D) * ES;
   const char *vbase = static_cast<const char *>(p.v) + (sp.k0 * p.sv + (int64_t)kv * D) * ES;
 
-  // this lane's query, and the rows of its wave
-  const int wrow = row0 + 32 * wave, mine = wrow + (lane & 31), row = min(mine, m.nq - 1);
-  const int wlast = min(wrow + 31, m.nq - 1);  // < wrow: a wave without queries
+  // this lane's query, and the keys that it sees
+  const int mine = row0 + 32 * wave + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
   Frag<BF16> q[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
   arrived(q);
   const float c = p.scale * kLog2e;
-  const int hi = m.hi(row), lo = m.lo(row);
-  // tiles that some query of the workgroup, and of the wave, sees; keys that
-  // every query of the workgroup, and of the wave, sees
+  // tiles that some query of the workgroup sees; keys that every one of them sees
   const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;  // hi = -1: none
-  const int w_lo = m.lo(min(wrow, m.nq - 1)), w_hi = wrow <= wlast ? m.hi(wlast) : -1;
   const int b_lo = m.lo(blast), b_hi = m.hi(row0);
-  const int all_lo = m.lo(max(wlast, 0)), all_hi = m.hi(min(wrow, m.nq - 1));
+  auto hides = [&](int key0) { return key0 < b_lo || key0 + KT - 1 > b_hi; };
 
   floatx16 acc[D / 32];
-#pragma unroll
-  for (int b = 0; b < D / 32; ++b) acc[b] = zero16();
-  float top = neg_inf(), sum = 0.f;
+  float top, sum;
+  Along<BF16, D> along;
+  Across<BF16, D> across;
+  along.init(lane);
+  across.init(lane);
+  const uint32_t at = lds_address(&sm);  // tile [i][j] from (2 i + j) TILE on
+  Dma<BF16, D, KT> ks, vs;
+  ks.init(p.sk * ES, tid);
+  vs.init(p.sv * ES, tid);
 
-  // One tile's products. masked (uniform): some query does not see some key.
-  auto step = [&](const char *kt, const char *vt, int key0, bool masked) __attribute__((always_inline)) {
-    floatx16 s[SUB];
+  // scores of one tile: keys as rows
+  auto scores = [&](floatx16 (&s)[SUB], uint32_t kt, int kk) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) s[u] = zero16();
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) s[u] = mma<BF16>(s[u], L::along(kt, 32 * u + (lane & 31), kk, h), q[kk]);
+    for (int u = 0; u < SUB; ++u) s[u] = mma<BF16>(kk ? s[u] : zero16(), along.read(kt, 32 * u, kk), q[kk]);
+  };
+  // One tile from its scores `s`; meanwhile the next tile's scores, so that matrix
+  // and vector instructions run side by side. masked (uniform): some query of the
+  // workgroup does not see some key.
+  auto step = [&](floatx16 (&s)[SUB], floatx16 (&next)[SUB], uint32_t vt, uint32_t next_kt, int key0,
+                  bool masked) __attribute__((always_inline)) {
     if (masked) {
       // key key0 + 32 u + row_of(i, h) is seen where `from` <= 32 u + row_of(i, 0) <= `to`
       const int from = lo - key0 - 4 * h, to = hi - key0 - 4 * h;
@@ -110,49 +108,83 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
         for (int i = 0; i < 16; ++i) acc[b][i] *= f;
     }
     const float base = top == neg_inf() ? 0.f : top;
+    // Probabilities by groups of 8 registers, each the operand of one step of the
+    // second product: the first half of them beside the next scores, each of the
+    // others beside the product two (SUB) groups before it.
+    auto weigh = [&](int group, int i) __attribute__((always_inline)) {
+      floatx16 &x = s[group / 2];
+      const int e = 8 * (group % 2) + i;
+      x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -base));
+      sum += x[e];
+    };
+    constexpr int STEPS = D / 16, BLOCKS = D / 32;
+    // the SIMD's other wave, in its own turn's vector part, lets the matrix products through
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int u = 0; u < SUB; ++u)
+    for (int kk = 0; kk < STEPS; ++kk) {
+      scores(next, next_kt, kk);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][i], c, -base));
-        sum += s[u][i];
+      for (int i = kk * 8 * SUB / STEPS; i < (kk + 1) * 8 * SUB / STEPS; ++i) weigh(i / 8, i % 8);
+    }
+#pragma unroll
+    for (int g = 0; g < 2 * SUB; ++g) {
+      // bf16: the probabilities' one rounding, 2^-9 of each at most
+      const Frag<BF16> w = operand<BF16>(s[g / 2], g % 2);
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) {
+        acc[b] = mma<BF16>(acc[b], across.read(vt, 16 * g, b), w);
+        if (g < SUB)
+#pragma unroll
+          for (int i = b * 8 / BLOCKS; i < (b + 1) * 8 / BLOCKS; ++i) weigh(g + SUB, i);
       }
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        // bf16: the probabilities' one rounding, 2^-9 of each at most
-        const Frag<BF16> w = operand<BF16>(s[u], g);
-#pragma unroll
-        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], L::across(vt, 32 * u + 16 * g, 32 * b, lane), w);
-      }
+    }
+    __builtin_amdgcn_s_setprio(0);
   };
 
-  if (t_lo < t_hi) {
-    Dma<BF16, D, KT> ks, vs;
-    ks.init(p.sk * ES, tid);
-    vs.init(p.sv * ES, tid);
+  for (bool careful = false;; careful = true) {
+    top = neg_inf();
+    sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) acc[b] = zero16();
+    if (t_lo >= t_hi) break;
     ks.load(sm.tile[0][0], kbase, t_lo * KT, m.nk, wave);
     vs.load(sm.tile[0][1], vbase, t_lo * KT, m.nk, wave);
+    if (t_lo + 1 < t_hi) ks.load(sm.tile[1][0], kbase, (t_lo + 1) * KT, m.nk, wave);
+    landed();
+    __syncthreads();
+    floatx16 s[2][SUB];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) scores(s[0], at, kk);
     // BUF: the tile's buffer, a constant, so that LDS addresses are a lane's own and an offset
     auto turn = [&](int t, auto buf) __attribute__((always_inline)) {
       constexpr int BUF = decltype(buf)::value;
       const int key0 = t * KT;
       landed();
-      __syncthreads();  // tile t is there, and nobody reads tile t - 1 any more
-      if (t + 1 < t_hi) {
-        ks.load(sm.tile[BUF ^ 1][0], kbase, key0 + KT, m.nk, wave);
-        vs.load(sm.tile[BUF ^ 1][1], vbase, key0 + KT, m.nk, wave);
-      }
-      char *kt = sm.tile[BUF][0], *vt = sm.tile[BUF][1];
-      const bool bad = (key0 < b_lo || key0 + KT - 1 > b_hi) && clean<BF16, D, KT>(vt, sm.notes, tid);
-      if (key0 <= w_hi && key0 + KT > w_lo) step(kt, vt, key0, key0 < all_lo || key0 + KT - 1 > all_hi);
-      if (bad) poison<BF16, D, KT>(acc, sm.notes, lo - key0, hi - key0, h);
+      __syncthreads();  // V of tile t and K of tile t + 1 are there, and nobody reads those before them any more
+      if (t + 1 < t_hi) vs.load(sm.tile[BUF ^ 1][1], vbase, key0 + KT, m.nk, wave);
+      if (t + 2 < t_hi) ks.load(sm.tile[BUF][0], kbase, key0 + 2 * KT, m.nk, wave);
+      const bool masked = hides(key0);
+      if (careful && masked) clean<BF16, TILE>(sm.tile[BUF][1], tid);
+      // (behind the last tile: scores of what the buffer holds, which nobody uses)
+      step(s[BUF], s[BUF ^ 1], at + (2 * BUF + 1) * TILE, at + 2 * (BUF ^ 1) * TILE, key0, masked);
     };
     for (int t = t_lo; t < t_hi; t += 2) {
       turn(t, std::integral_constant<int, 0>{});
       if (t + 1 < t_hi) turn(t + 1, std::integral_constant<int, 1>{});
     }
+    if (careful) {
+#pragma unroll 1
+      for (int t = t_lo; t < t_hi; ++t) {
+        if (!hides(t * KT)) continue;
+        __syncthreads();
+        vs.load(sm.tile[0][1], vbase, t * KT, m.nk, wave);
+        landed();
+        __syncthreads();
+        poison<BF16, D, KT>(acc, sm.tile[0][1], lo - t * KT, hi - t * KT, h);
+      }
+      break;
+    }
+    if (!any_wave(any_odd(acc), sm.said, tid)) break;
   }
 
   if (mine >= m.nq) return;
@@ -165,10 +197,9 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
 
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
   const size_t tiles = attention_tiles(p.cu_q ? p.B : 1, p.Tq, p.cu_q != nullptr);
-  const size_t total = tiles * (p.cu_q ? 1 : (size_t)p.B) * (size_t)p.H;
-  if (!total) return hipSuccess;
-  const unsigned grid = (unsigned)((total + 7) / 8 * 8);
-  attention_forward_kernel<BF16, D><<<grid, 256, 0, stream>>>(p, (unsigned)total, (unsigned)tiles);
+  const size_t units = (p.cu_q ? 1 : (size_t)p.B) * (size_t)p.H;
+  if (!tiles || !units) return hipSuccess;
+  attention_forward_kernel<BF16, D><<<(unsigned)(tiles * units), 256, 0, stream>>>(p, (unsigned)units);
   return hipGetLastError();
 }
 

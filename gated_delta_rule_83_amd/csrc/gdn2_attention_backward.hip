@@ -20,24 +20,25 @@ using namespace attn;
 
 // ---------------------------------------------------------------- dq
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256, BF16 ? 2 : 1) attention_dq_kernel(const AttentionArgs p, unsigned total, unsigned tiles) {
+__global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
-  constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4;
+  constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4, TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
-    char tile[2][2][KT * L::ROW];
-    Odd<BF16, D, KT> notes;
+    char tile[2][2][TILE];  // first: within the 64 KB that m0 addresses
+    uint32_t said[4];
   } sm;
-  unsigned unit, tile;
-  if (!find_work(total, tiles, &unit, &tile)) return;
+  unsigned unit, rank;
+  find_work(units, &unit, &rank);
+  const int tile = (int)(gridDim.x / units - 1 - rank);  // causal: the last block sees most
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block(p.cu_q, p.B, p.Tq, (int)tile, &seq, &row0)) return;
+    if (!find_block(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
     head = (int)(unit % (unsigned)p.H);
-    row0 = (int)tile * kAttnRows;
+    row0 = tile * kAttnRows;
   }
   const Span sp = span_of(p, seq, head);
   const Mask m = sp.m;
@@ -46,16 +47,15 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) attention_dq_kernel(const A
   const char *kbase = static_cast<const char *>(p.k) + (sp.k0 * p.sk + (int64_t)kv * D) * ES;
   const char *vbase = static_cast<const char *>(p.v) + (sp.k0 * p.sv + (int64_t)kv * D) * ES;
 
-  const int wrow = row0 + 32 * wave, mine = wrow + (lane & 31), row = min(mine, m.nq - 1);
-  const int wlast = min(wrow + 31, m.nq - 1);
-  const int64_t at = ((sp.q0 + row) * (int64_t)p.H + head) * D * ES;  // the row in o, dO and dq
+  const int mine = row0 + 32 * wave + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
+  const int64_t place = ((sp.q0 + row) * (int64_t)p.H + head) * D * ES;  // the row in o, dO and dq
   Frag<BF16> q[D / 16], g[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
-  load_row<BF16, D>(g, static_cast<const char *>(p.dO) + at, h);
+  load_row<BF16, D>(g, static_cast<const char *>(p.dO) + place, h);
   float delta = 0.f;
   {
     Frag<BF16> o[D / 16];
-    load_row<BF16, D>(o, static_cast<const char *>(p.o_in) + at, h);
+    load_row<BF16, D>(o, static_cast<const char *>(p.o_in) + place, h);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -71,205 +71,299 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) attention_dq_kernel(const A
     p.delta[sp.rows + mine] = delta;
     p.lse[sp.rows + mine] = lse;
   }
-  const int hi = m.hi(row), lo = m.lo(row);
   const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;
-  const int w_lo = m.lo(min(wrow, m.nq - 1)), w_hi = wrow <= wlast ? m.hi(wlast) : -1;
   const int b_lo = m.lo(blast), b_hi = m.hi(row0);
-  const int all_lo = m.lo(max(wlast, 0)), all_hi = m.hi(min(wrow, m.nq - 1));
+  auto hides = [&](int key0) { return key0 < b_lo || key0 + KT - 1 > b_hi; };
 
   floatx16 acc[D / 32];
+  Along<BF16, D> along;
+  Across<BF16, D> across;
+  along.init(lane);
+  across.init(lane);
+  const uint32_t at = lds_address(&sm);  // tile [i][j] from (2 i + j) TILE on
+  Dma<BF16, D, KT> ks, vs;
+  ks.init(p.sk * ES, tid);
+  vs.init(p.sv * ES, tid);
+
+  // ds of 32 keys
+  auto part = [&](Frag<BF16> (&ds)[2], uint32_t kt, uint32_t vt, int u, int key0, auto masked) __attribute__((always_inline)) {
+    floatx16 s = zero16(), dp = zero16();
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b) acc[b] = zero16();
-  if (t_lo < t_hi) {
-    Dma<BF16, D, KT> ks, vs;
-    ks.init(p.sk * ES, tid);
-    vs.init(p.sv * ES, tid);
-    ks.load(sm.tile[t_lo & 1][0], kbase, t_lo * KT, m.nk, wave);
-    vs.load(sm.tile[t_lo & 1][1], vbase, t_lo * KT, m.nk, wave);
-    for (int t = t_lo; t < t_hi; ++t) {
+    for (int kk = 0; kk < D / 16; ++kk) {
+      s = mma<BF16>(s, along.read(kt, 32 * u, kk), q[kk]);
+      dp = mma<BF16>(dp, along.read(vt, 32 * u, kk), g[kk]);
+    }
+    const int from = lo - key0 - 4 * h, to = hi - key0 - 4 * h;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (dp[i] - delta);
+      if constexpr (decltype(masked)::value)
+        if (32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to) s[i] = 0.f;
+    }
+    // bf16: one rounding of each ds
+    ds[0] = operand<BF16>(s, 0);
+    ds[1] = operand<BF16>(s, 1);
+  };
+  auto product = [&](const Frag<BF16> (&ds)[2], uint32_t kt, int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(kt, 32 * u + 16 * e, b), ds[e]);
+  };
+
+  for (bool careful = false;; careful = true) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) acc[b] = zero16();
+    if (t_lo >= t_hi) break;
+    ks.load(sm.tile[0][0], kbase, t_lo * KT, m.nk, wave);
+    vs.load(sm.tile[0][1], vbase, t_lo * KT, m.nk, wave);
+    auto turn = [&](int t, auto buf) __attribute__((always_inline)) {
+      constexpr int BUF = decltype(buf)::value;
       const int key0 = t * KT;
       landed();
-      __syncthreads();
+      __syncthreads();  // tile t is there, and nobody reads tile t - 1 any more
       if (t + 1 < t_hi) {
-        ks.load(sm.tile[(t + 1) & 1][0], kbase, key0 + KT, m.nk, wave);
-        vs.load(sm.tile[(t + 1) & 1][1], vbase, key0 + KT, m.nk, wave);
+        ks.load(sm.tile[BUF ^ 1][0], kbase, key0 + KT, m.nk, wave);
+        vs.load(sm.tile[BUF ^ 1][1], vbase, key0 + KT, m.nk, wave);
       }
-      char *kt = sm.tile[t & 1][0];
-      const char *vt = sm.tile[t & 1][1];
-      const bool live = key0 <= w_hi && key0 + KT > w_lo;
+      const uint32_t kt = at + 2 * BUF * TILE, vt = kt + TILE;
       Frag<BF16> ds[SUB][2];
-      if (live) {
-        const bool masked = key0 < all_lo || key0 + KT - 1 > all_hi;
-        const int from = lo - key0 - 4 * h, to = hi - key0 - 4 * h;
+      if (hides(key0)) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) part(ds[u], kt, vt, u, key0, std::true_type{});
+        if (careful) {  // the scores take K as it is, the product without its odd values
+          __syncthreads();
+          clean<BF16, TILE>(sm.tile[BUF][0], tid);
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) product(ds[u], kt, u);
+      } else {
+        // each 32 keys' product beside the next ones' scores
+        part(ds[0], kt, vt, 0, key0, std::false_type{});
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          floatx16 s = zero16(), dp = zero16();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) s = mma<BF16>(s, L::along(kt, 32 * u + (lane & 31), kk, h), q[kk]);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) dp = mma<BF16>(dp, L::along(vt, 32 * u + (lane & 31), kk, h), g[kk]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (dp[i] - delta);
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to) s[i] = 0.f;
-          }
-          // bf16: one rounding of each ds
-          ds[u][0] = operand<BF16>(s, 0);
-          ds[u][1] = operand<BF16>(s, 1);
+          if (u + 1 < SUB) part(ds[u + 1], kt, vt, u + 1, key0, std::false_type{});
+          product(ds[u], kt, u);
         }
       }
-      const bool bad = (key0 < b_lo || key0 + KT - 1 > b_hi) && clean<BF16, D, KT>(kt, sm.notes, tid);
-      if (live) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], L::across(kt, 32 * u + 16 * e, 32 * b, lane), ds[u][e]);
-      }
-      if (bad) poison<BF16, D, KT>(acc, sm.notes, lo - key0, hi - key0, h);
+    };
+    for (int t = t_lo; t < t_hi; t += 2) {
+      turn(t, std::integral_constant<int, 0>{});
+      if (t + 1 < t_hi) turn(t + 1, std::integral_constant<int, 1>{});
     }
+    if (careful) {
+#pragma unroll 1
+      for (int t = t_lo; t < t_hi; ++t) {
+        if (!hides(t * KT)) continue;
+        __syncthreads();
+        ks.load(sm.tile[0][0], kbase, t * KT, m.nk, wave);
+        landed();
+        __syncthreads();
+        poison<BF16, D, KT>(acc, sm.tile[0][0], lo - t * KT, hi - t * KT, h);
+      }
+      break;
+    }
+    if (!any_wave(any_odd(acc), sm.said, tid)) break;
   }
-  if (mine < m.nq) store_row<BF16, D>(static_cast<char *>(p.dq) + at, acc, p.scale, h);
+  if (mine < m.nq) store_row<BF16, D>(static_cast<char *>(p.dq) + place, acc, p.scale, h);
 }
 
 // ---------------------------------------------------------------- dk, dv
+// 128 keys, 32 a pair of waves. The one keeps K and dv: scores, probabilities,
+// dv += dO^T p; the other V and dk: dp, ds, dk += Q^T ds, one tile of queries
+// behind, with the probabilities from LDS (in fp32: a rounding of them would
+// stand beside the one of ds). So both have two products a tile and registers
+// for two waves a SIMD, one of each kind; with all four products and both
+// accumulators in one wave there is one a SIMD, whose vector instructions keep
+// the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us).
 template <bool BF16, int D>
-__global__ void __launch_bounds__(256, 1) attention_dkv_kernel(const AttentionArgs p, unsigned total, unsigned tiles) {
+__global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
-  constexpr int QT = 32, ES = BF16 ? 2 : 4;
+  constexpr int QT = 32, ES = BF16 ? 2 : 4, TILE = QT * L::ROW, RING = 3;
+  constexpr int PROBS = 32 * 32 * 4;
   __shared__ __attribute__((aligned(16))) struct {
-    char tile[2][2][QT * L::ROW];
-    float stat[2][2][64];  // lse in powers of two and delta of a tile's rows (64 lanes land, 32 are used)
-    Odd<BF16, D, QT> notes[2];
+    char tile[RING][2][TILE];  // Q, dO
+    float stat[RING][2][64];   // lse in powers of two and delta of a tile's rows (64 lanes land, 32 are used)
+    char probs[RING][4][PROBS];
+    uint32_t said[8];
   } sm;
-  unsigned unit, tile;
-  if (!find_work(total, tiles, &unit, &tile)) return;
+  unsigned unit, rank;
+  find_work(units, &unit, &rank);
+  const int tile = (int)rank;  // causal: the first keys are seen most
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool second = wave >= 4;  // keeps V and dk
+  const int pair = wave & 3;
   const int group = p.H / p.Hkv, share = group / p.parts;  // query heads of a key head, and of this workgroup
   int seq, row0;
-  const int part = (int)(unit % (unsigned)p.parts);
+  const int slice = (int)(unit % (unsigned)p.parts);
   unsigned kvu = unit / (unsigned)p.parts;
   if (p.cu_q) {
-    if (!find_block(p.cu_k, p.B, p.Tk, (int)tile, &seq, &row0)) return;
+    if (!find_block(p.cu_k, p.B, p.Tk, tile, &seq, &row0)) return;
   } else {
     seq = (int)(kvu / (unsigned)p.Hkv);
     kvu %= (unsigned)p.Hkv;
-    row0 = (int)tile * kAttnRows;
+    row0 = tile * kAttnRows;
   }
-  const int kv = (int)kvu, head0 = kv * group + part * share;
+  const int kv = (int)kvu, head0 = kv * group + slice * share;
   const Span sp = span_of(p, seq, head0);
   const Mask m = sp.m;
   if (row0 >= m.nk) return;
 
-  const int wrow = row0 + 32 * wave, mine = wrow + (lane & 31), row = min(mine, m.nk - 1);
-  const int wlast = min(wrow + 31, m.nk - 1);
-  Frag<BF16> k[D / 16], v[D / 16];
-  load_row<BF16, D>(k, static_cast<const char *>(p.k) + ((sp.k0 + row) * p.sk + (int64_t)kv * D) * ES, h);
-  load_row<BF16, D>(v, static_cast<const char *>(p.v) + ((sp.k0 + row) * p.sv + (int64_t)kv * D) * ES, h);
-  arrived(k);
-  arrived(v);
+  const int mine = row0 + 32 * pair + (lane & 31), row = min(mine, m.nk - 1);
+  Frag<BF16> kept[D / 16];
+  load_row<BF16, D>(kept, static_cast<const char *>(second ? p.v : p.k) + ((sp.k0 + row) * (second ? p.sv : p.sk) + (int64_t)kv * D) * ES, h);
+  arrived(kept);
   const float c = p.scale * kLog2e;
   const int first = m.first(row), last = m.last(row);
-  // query tiles that some key of the workgroup, and of the wave, is seen from;
-  // queries that see every key of them
+  // query tiles that some key of the workgroup is seen from; queries that see every one of them
   const int blast = min(row0 + kAttnRows - 1, m.nk - 1);
   const int t_lo = m.first(row0) / QT, t_hi = (m.last(blast) + QT) / QT;
-  const int w_lo = m.first(min(wrow, m.nk - 1)), w_hi = wrow <= wlast ? m.last(wlast) : -1;
   const int b_lo = m.first(blast), b_hi = m.last(row0);
-  const int all_lo = m.first(max(wlast, 0)), all_hi = m.last(min(wrow, m.nk - 1));
+  auto hides = [&](int q0) { return q0 < b_lo || q0 + QT - 1 > b_hi; };
 
-  floatx16 dk[D / 32], dv[D / 32];
+  floatx16 acc[D / 32];
+  Along<BF16, D> along;
+  Across<BF16, D> across;
+  along.init(lane);
+  across.init(lane);
+  const uint32_t at = lds_address(&sm), stats = lds_address(&sm.stat), probs = lds_address(&sm.probs) + pair * PROBS + lane * 16;
+  const int nt = t_hi - t_lo, turns = nt > 0 ? nt * share : 0;
+  // the first waves fetch Q, the second dO
+  Dma<BF16, D, QT> rows;
+  rows.init((second ? (int64_t)p.H * D : p.sq) * ES, tid & 255);
+  const char *base = second ? static_cast<const char *>(p.dO) + (sp.q0 * (int64_t)p.H + head0) * D * ES
+                            : static_cast<const char *>(p.q) + (sp.q0 * p.sq + (int64_t)head0 * D) * ES;
+  // tile t of head head0 + hd into buffer `to`
+  auto fetch = [&](int hd, int t, int to) __attribute__((always_inline)) {
+    const int r0 = t * QT;
+    rows.load(sm.tile[to][second], base + (int64_t)hd * D * ES, r0, m.nq, pair);
+    if (pair == 0) {
+      const float *from = (second ? p.delta : p.lse) + sp.rows + (int64_t)hd * p.Tq + r0;
+      dma<4>(reinterpret_cast<const char *>(from), (uint32_t)min(m.nq - r0, QT) * 4, lane * 4, lds_address(sm.stat[to][second]));
+    }
+  };
+  // whether the query of register i does not see this lane's key
+  auto outside = [&](int q0, int i) {
+    const int from = first - q0 - 4 * h, to = last - q0 - 4 * h;
+    return row_of(i, 0) < from || row_of(i, 0) > to;
+  };
+
+  auto scores = [&](int q0, int buf, auto masked) __attribute__((always_inline)) {
+    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 16 * h, pt = probs + buf * 4 * PROBS;
+    floatx16 s = zero16();
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b) dk[b] = dv[b] = zero16();
-  const int nt = t_hi - t_lo;
-  if (nt > 0) {
-    Dma<BF16, D, QT> qs, gs;
-    qs.init(p.sq * ES, tid);
-    gs.init((int64_t)p.H * D * ES, tid);
-    // tile t of head head0 + hd into buffer `to`
-    auto fetch = [&](int hd, int t, int to) {
-      const int head = head0 + hd, r0 = t * QT;
-      qs.load(sm.tile[to][0], static_cast<const char *>(p.q) + (sp.q0 * p.sq + (int64_t)head * D) * ES, r0, m.nq, wave);
-      gs.load(sm.tile[to][1], static_cast<const char *>(p.dO) + (sp.q0 * (int64_t)p.H + head) * D * ES, r0, m.nq, wave);
-      if (wave < 2) {
-        const float *from = (wave ? p.delta : p.lse) + sp.rows + (int64_t)hd * p.Tq + r0;
-        dma<4>(reinterpret_cast<const char *>(from), (uint32_t)min(m.nq - r0, QT) * 4, lane * 4, lds_address(sm.stat[to][wave]));
+    for (int kk = 0; kk < D / 16; ++kk) s = mma<BF16>(s, along.read(qt, 0, kk), kept[kk]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const floatx4 l = lds_read<floatx4>(st + 4 * row_of(i, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -l[e]));
+    }
+    if constexpr (decltype(masked)::value) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (outside(q0, i)) s[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<__attribute__((address_space(3))) floatx4 *>((uintptr_t)(pt + i * 256)) = floatx4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const Frag<BF16> w = operand<BF16>(s, e);  // bf16: one rounding of each p
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(gt, 16 * e, b), w);
+    }
+  };
+  auto slopes = [&](int q0, int buf, auto masked) __attribute__((always_inline)) {
+    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 256 + 16 * h, pt = probs + buf * 4 * PROBS;
+    floatx16 s = zero16();
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) s = mma<BF16>(s, along.read(gt, 0, kk), kept[kk]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const floatx4 d = lds_read<floatx4>(st + 4 * row_of(i, 0)), w = lds_read<floatx4>(pt + i * 256);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i + e] = w[e] * (s[i + e] - d[e]);
+    }
+    if constexpr (decltype(masked)::value) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (outside(q0, i)) s[i] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const Frag<BF16> w = operand<BF16>(s, e);  // bf16: one rounding of each ds
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(qt, 16 * e, b), w);
+    }
+  };
+
+  for (bool careful = false;; careful = true) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) acc[b] = zero16();
+    if (turns == 0) break;
+    fetch(0, t_lo, 0);
+    // turn i: tile i for the first wave of a pair, tile i - 1 for the second; tile i + 1 on its way. Each kind has
+    // a loop of its own with the same barriers.
+    auto walk = [&](auto kind) __attribute__((always_inline)) {
+      constexpr bool SECOND = decltype(kind)::value;
+      int t = t_lo, ahead_hd = 0, ahead = t_lo;
+      auto turn = [&](int i, auto buf) __attribute__((always_inline)) {
+        constexpr int BUF = decltype(buf)::value, BEFORE = (BUF + RING - 1) % RING, NEXT = (BUF + 1) % RING;
+        landed();
+        __syncthreads();  // tile i and the probabilities of tile i - 1 are there; nobody reads tile i - 2 any more
+        if (i + 1 < turns) {
+          if (++ahead == t_hi) ahead = t_lo, ++ahead_hd;
+          fetch(ahead_hd, ahead, NEXT);
+        }
+        if (careful && i < turns && hides((t_lo + i % nt) * QT)) {
+          // (lse and delta of a row hold what its odd values made of it)
+          clean<BF16, TILE>(sm.tile[BUF][0], tid);
+          clean<BF16, TILE>(sm.tile[BUF][1], tid);
+        }
+        if constexpr (SECOND) {
+          if (i == 0) return;
+          if (hides(t * QT)) slopes(t * QT, BEFORE, std::true_type{});
+          else slopes(t * QT, BEFORE, std::false_type{});
+        } else {
+          if (i == turns) return;
+          if (hides(t * QT)) scores(t * QT, BUF, std::true_type{});
+          else scores(t * QT, BUF, std::false_type{});
+        }
+        if (++t == t_hi) t = t_lo;
+      };
+      for (int i = 0; i <= turns; i += RING) {
+        turn(i, std::integral_constant<int, 0>{});
+        if (i + 1 <= turns) turn(i + 1, std::integral_constant<int, 1>{});
+        if (i + 2 <= turns) turn(i + 2, std::integral_constant<int, 2>{});
       }
     };
-    fetch(0, t_lo, 0);
-    int hd = 0, t = t_lo;
-    for (int it = 0; it < nt * share; ++it) {
-      const int q0 = t * QT, buf = it & 1;
-      landed();
-      __syncthreads();
-      if (++t == t_hi) t = t_lo, ++hd;
-      if (hd < share) fetch(hd, t, buf ^ 1);
-      char *qt = sm.tile[buf][0], *gt = sm.tile[buf][1];
-      const float *ls = sm.stat[buf][0], *dl = sm.stat[buf][1];
-      const bool live = q0 <= w_hi && q0 + QT > w_lo;
-      Frag<BF16> pr[2], ds[2];
-      if (live) {
-        const bool masked = q0 < all_lo || q0 + QT - 1 > all_hi;
-        floatx16 s = zero16(), dp = zero16();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) s = mma<BF16>(s, L::along(qt, lane & 31, kk, h), k[kk]);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) dp = mma<BF16>(dp, L::along(gt, lane & 31, kk, h), v[kk]);
-        const int from = first - q0 - 4 * h, to = last - q0 - 4 * h;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const floatx4 l4 = *reinterpret_cast<const floatx4 *>(ls + row_of(i, h));
-          const floatx4 d4 = *reinterpret_cast<const floatx4 *>(dl + row_of(i, h));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -l4[e]));
-            dp[i + e] = s[i + e] * (dp[i + e] - d4[e]);
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (row_of(i, 0) < from || row_of(i, 0) > to) s[i] = dp[i] = 0.f;
-        }
-        // bf16: one rounding of each p and ds
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          pr[e] = operand<BF16>(s, e);
-          ds[e] = operand<BF16>(dp, e);
-        }
+    if (second) walk(std::true_type{});
+    else walk(std::false_type{});
+    if (careful) {
+#pragma unroll 1
+      for (int i = 0; i < turns; ++i) {
+        const int q0 = (t_lo + i % nt) * QT;
+        if (!hides(q0)) continue;
+        __syncthreads();
+        fetch(i / nt, t_lo + i % nt, 0);
+        landed();
+        __syncthreads();
+        poison<BF16, D, QT>(acc, sm.tile[0][second ? 0 : 1], first - q0, last - q0, h);
       }
-      bool bad_q = false, bad_g = false;
-      if (q0 < b_lo || q0 + QT - 1 > b_hi) {
-        bad_q = clean<BF16, D, QT>(qt, sm.notes[0], tid);
-        bad_g = clean<BF16, D, QT>(gt, sm.notes[1], tid);
-      }
-      if (live) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int b = 0; b < D / 32; ++b) {
-            dv[b] = mma<BF16>(dv[b], L::across(gt, 16 * e, 32 * b, lane), pr[e]);
-            dk[b] = mma<BF16>(dk[b], L::across(qt, 16 * e, 32 * b, lane), ds[e]);
-          }
-      }
-      if (bad_q) poison<BF16, D, QT>(dk, sm.notes[0], first - q0, last - q0, h);
-      if (bad_g) poison<BF16, D, QT>(dv, sm.notes[1], first - q0, last - q0, h);
+      break;
     }
+    if (!any_wave(any_odd(acc), sm.said, tid)) break;
   }
   if (mine >= m.nk) return;
+  const float f = second ? p.scale : 1.f;
+  const int64_t to = ((sp.k0 + mine) * (int64_t)p.Hkv + kv) * D;
   if (p.parts == 1) {
-    const int64_t at = ((sp.k0 + mine) * (int64_t)p.Hkv + kv) * D * ES;
-    store_row<BF16, D>(static_cast<char *>(p.dk) + at, dk, p.scale, h);
-    store_row<BF16, D>(static_cast<char *>(p.dv) + at, dv, 1.f, h);
+    store_row<BF16, D>(static_cast<char *>(second ? p.dk : p.dv) + to * ES, acc, f, h);
   } else {
     const int64_t n = (int64_t)(p.cu_q ? 1 : p.B) * p.Tk * p.Hkv * D;
-    char *to = reinterpret_cast<char *>(p.partial + 2 * part * n + ((sp.k0 + mine) * (int64_t)p.Hkv + kv) * D);
-    store_row<false, D>(to, dk, p.scale, h);
-    store_row<false, D>(to + n * 4, dv, 1.f, h);
+    store_row<false, D>(reinterpret_cast<char *>(p.partial + (2 * slice + !second) * n + to), acc, f, h);
   }
 }
 
@@ -312,19 +406,18 @@ __global__ void __launch_bounds__(256) attention_outside_kernel(const AttentionA
 
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
   const bool packed = p.cu_q != nullptr;
-  const size_t units = packed ? 1 : (size_t)p.B;
-  const size_t tq = attention_tiles(packed ? p.B : 1, p.Tq, packed), nq = tq * units * (size_t)p.H;
-  if (nq) {
-    attention_dq_kernel<BF16, D><<<(unsigned)((nq + 7) / 8 * 8), 256, 0, stream>>>(p, (unsigned)nq, (unsigned)tq);
+  const size_t seqs = packed ? 1 : (size_t)p.B;
+  const size_t tq = attention_tiles(packed ? p.B : 1, p.Tq, packed), uq = seqs * (size_t)p.H;
+  if (tq) {
+    attention_dq_kernel<BF16, D><<<(unsigned)(tq * uq), 256, 0, stream>>>(p, (unsigned)uq);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  const size_t tk = attention_tiles(packed ? p.B : 1, p.Tk, packed), nk = tk * units * (size_t)p.Hkv * (size_t)p.parts;
-  if (nk) {
-    attention_dkv_kernel<BF16, D><<<(unsigned)((nk + 7) / 8 * 8), 256, 0, stream>>>(p, (unsigned)nk, (unsigned)tk);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
-  if (nk && p.parts > 1) {
-    const int64_t n = (int64_t)units * p.Tk * p.Hkv * D;
+  const size_t tk = attention_tiles(packed ? p.B : 1, p.Tk, packed), uk = seqs * (size_t)p.Hkv * (size_t)p.parts;
+  if (!tk) return hipSuccess;
+  attention_dkv_kernel<BF16, D><<<(unsigned)(tk * uk), 512, 0, stream>>>(p, (unsigned)uk);
+  if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if (p.parts > 1) {
+    const int64_t n = (int64_t)seqs * p.Tk * p.Hkv * D;
     attention_join_kernel<BF16><<<(unsigned)((n / 4 + 255) / 256), 256, 0, stream>>>(p, n);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

@@ -77,42 +77,77 @@ template <bool BF16, int D> struct Tile {
   }
   static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swizzle(r)) << 4); }
 
-  // row r, values 16 kk + 8 h ..: an operand whose contracted axis runs along the rows
-  static __device__ __forceinline__ Frag<BF16> along(const char *t, int r, int kk, int h) {
+};
+
+template <class V> __device__ __forceinline__ V lds_read(uint32_t at) {
+  return *reinterpret_cast<__attribute__((address_space(3))) const V *>((uintptr_t)at);
+}
+
+// A lane's places in a tile. Rows 16 apart are exchanged alike, so the places of
+// rows r .. r + 15 serve all the others: what a read adds is a constant.
+template <bool BF16, int D> struct Along {  // rows as rows or columns of an operand, contracted along them
+  using L = Tile<BF16, D>;
+  uint32_t off[D / 16];
+  __device__ __forceinline__ void init(int lane) {
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) off[kk] = L::at(r, BF16 ? 2 * kk + h : 4 * kk + 2 * h);
+  }
+  // row r0 + (lane & 31), values 16 kk + 8 h ..; tile: LDS address; r0 a multiple of 16
+  __device__ __forceinline__ Frag<BF16> read(uint32_t tile, int r0, int kk) const {
     if constexpr (BF16) {
-      return Frag<true>{*reinterpret_cast<const bf16x8 *>(t + at(r, 2 * kk + h))};
+      return Frag<true>{lds_read<bf16x8>(off[kk] + (tile + r0 * L::ROW))};
     } else {
-      const floatx4 x = *reinterpret_cast<const floatx4 *>(t + at(r, 4 * kk + 2 * h));
-      const floatx4 y = *reinterpret_cast<const floatx4 *>(t + at(r, 4 * kk + 2 * h + 1));
+      const floatx4 x = lds_read<floatx4>(off[kk] + (tile + r0 * L::ROW)), y = lds_read<floatx4>((off[kk] ^ 16) + (tile + r0 * L::ROW));
       return Frag<false>{__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)};
     }
   }
+};
 
-  // column c0 + (lane & 31), slots j = rows r0 + 8 (j / 4) + 4 h + j % 4: an
-  // operand whose contracted axis runs across the rows. bf16: in a transposing
-  // read lane 4 a + b of 16 receives value b of the 8 bytes that lanes a, a + 4,
-  // a + 8 and a + 12 address, so lane j addresses row j / 4, columns 4 (j % 4).
-  static __device__ __forceinline__ Frag<BF16> across(const char *t, int r0, int c0, int lane) {
+// Columns, contracted across the rows: slot j is row 8 (j / 4) + 4 h + j % 4.
+// bf16: in a transposing read lane 4 a + b of 16 receives value b of the 8 bytes
+// that lanes a, a + 4, a + 8 and a + 12 address, so lane j addresses row j / 4,
+// columns 4 (j % 4).
+template <bool BF16, int D> struct Across {
+  using L = Tile<BF16, D>;
+  uint32_t off[D / 32][BF16 ? 2 : 1];
+  __device__ __forceinline__ void init(int lane) {
     const int h = lane >> 5;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) {
+      if constexpr (BF16) {
+        const int col = 32 * b + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), r = 4 * h + ((lane >> 2) & 3);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) off[b][e] = L::at(r + 8 * e, col >> 3) + 2 * (col & 7);
+      } else {
+        const int col = 32 * b + (lane & 31);
+        off[b][0] = L::at(4 * h, col >> 2) + 4 * (col & 3);
+      }
+    }
+  }
+  // columns 32 b + (lane & 31), rows r0 .. r0 + 15
+  __device__ __forceinline__ Frag<BF16> read(uint32_t tile, int r0, int b) const {
+    const uint32_t at = tile + r0 * L::ROW;
     if constexpr (BF16) {
-      const int col = c0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), r = r0 + 4 * h + ((lane >> 2) & 3);
-      auto rd = [&](int row) {
-        const char *src = t + at(row, col >> 3) + 2 * (col & 7);
-        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) v4i16 *)(__attribute__((address_space(3))) const char *)src));
+      auto rd = [&](uint32_t x) {
+        return __builtin_bit_cast(
+            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16 *)(uintptr_t)(x + at)));
       };
-      return Frag<true>{__builtin_shufflevector(rd(r), rd(r + 8), 0, 1, 2, 3, 4, 5, 6, 7)};
+      return Frag<true>{__builtin_shufflevector(rd(off[b][0]), rd(off[b][1]), 0, 1, 2, 3, 4, 5, 6, 7)};
     } else {
-      const int col = c0 + (lane & 31);
       Frag<false> f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f.v[j] = *reinterpret_cast<const float *>(t + at(r0 + 8 * (j >> 2) + 4 * h + (j & 3), col >> 2) + 4 * (col & 3));
+      for (int j = 0; j < 8; ++j) {
+        constexpr int ROW = L::ROW;
+        const int r = 8 * (j >> 2) + (j & 3);  // on top of 4 h: bits of their own, in the exchange too
+        f.v[j] = lds_read<float>((off[b][0] ^ (L::swizzle(r) << 4)) + (at + r * ROW));
+      }
       return f;
     }
   }
 };
 
+// ---------------------------------------------------------------- tiles from memory
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
 
 // R rows straight from memory into a tile: 16 bytes a lane, which land in LDS
@@ -202,60 +237,54 @@ template <bool BF16, int D> __device__ __forceinline__ void store_row(char *row,
 // ---------------------------------------------------------------- values in hidden places
 // In a tile of which some places are hidden, an infinity or NaN there must leave
 // nothing, though 0 times it is NaN, and one in a place that a row sees must
-// make that row's result NaN in its column. So the workgroup looks through such
-// a tile first; where it holds one (rare), it is replaced by zero and noted, a
-// byte for 16 bytes of the tile, and poison() puts NaN into the results that
-// see it.
+// make that row's result NaN in its column. A workgroup computes as if there
+// were none; if a result is no number in the end (rare), it computes once more
+// with such tiles' odd values replaced by zero (clean), then looks through those
+// tiles again and puts NaN into the results that see one (poison).
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {  // sign bits of the bf16 halves that are no number
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 __device__ __forceinline__ bool odd(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
 
-// Notes of one tile, and a word of each wave.
-template <bool BF16, int D, int R> struct Odd {
-  uint8_t note[R * Tile<BF16, D>::CHUNKS];
-  uint32_t wave[4];
-};
-
-// The whole workgroup (256 threads) calls; true: the tile held some, and `o` says where.
-template <bool BF16, int D, int R> __device__ __forceinline__ bool clean(char *t, Odd<BF16, D, R> &o, int tid) {
-  constexpr int N = R * Tile<BF16, D>::CHUNKS;
-  bool f = false;
-#pragma unroll
-  for (int i = 0; i < N / 256; ++i) {
-    const uintx4 w = *reinterpret_cast<const uintx4 *>(t + (tid + i * 256) * 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f |= BF16 ? odd_halves(w[j]) != 0 : odd(w[j]);
-  }
+// Whether any of the workgroup's waves says so. `said`: a word of each.
+template <int WAVES> __device__ __forceinline__ bool any_wave(bool f, uint32_t (&said)[WAVES], int tid) {
   const bool any = __any(f);
-  if ((tid & 63) == 0) o.wave[tid >> 6] = any;
+  if ((tid & 63) == 0) said[tid >> 6] = any;
   __syncthreads();
-  if (!uniform(o.wave[0] | o.wave[1] | o.wave[2] | o.wave[3])) return false;
+  uint32_t x = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) x |= said[w];
+  return uniform(x) != 0;
+}
+
+// Zeros for a tile's odd values. The whole workgroup calls, and nobody reads the tile meanwhile.
+template <bool BF16, int BYTES> __device__ __forceinline__ void clean(char *t, int tid) {
 #pragma unroll 1
-  for (int i = tid; i < N; i += 256) {
-    uintx4 w = *reinterpret_cast<const uintx4 *>(t + i * 16);
-    uint32_t bits = 0;
+  for (int i = tid * 16; i < BYTES; i += blockDim.x * 16) {
+    uintx4 w = *reinterpret_cast<const uintx4 *>(t + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (BF16) {
-        const uint32_t m = odd_halves(w[j]);
-        bits |= ((m >> 15) & 1u) << (2 * j) | (m >> 31) << (2 * j + 1);
-        w[j] &= ~((m >> 15) * 0xffffu);
-      } else if (odd(w[j])) {
-        bits |= 1u << j;
-        w[j] = 0;
-      }
+      if constexpr (BF16) w[j] &= ~((odd_halves(w[j]) >> 15) * 0xffffu);
+      else if (odd(w[j])) w[j] = 0;
     }
-    o.note[i] = (uint8_t)bits;
-    *reinterpret_cast<uintx4 *>(t + i * 16) = w;
+    *reinterpret_cast<uintx4 *>(t + i) = w;
   }
   __syncthreads();
-  return true;
+}
+
+template <int N> __device__ __forceinline__ bool any_odd(const floatx16 (&acc)[N]) {
+  bool f = false;
+#pragma unroll
+  for (int b = 0; b < N; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f |= odd(__float_as_uint(acc[b][i]));
+  return f;
 }
 
 // Rows first .. last of the tile are those this lane's column sees.
 template <bool BF16, int D, int R>
-__device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const Odd<BF16, D, R> &o, int first, int last, int h) {
+__device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const char *t, int first, int last, int h) {
+  using L = Tile<BF16, D>;
   first = max(first, 0);
   last = min(last, R - 1);
 #pragma unroll 1
@@ -264,11 +293,18 @@ __device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const Odd<BF16, 
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        const int col = 32 * b + row_of(i, h);
-        const uint32_t bits = BF16 ? o.note[Tile<BF16, D>::at(r, col >> 3) >> 4] >> (col & 4) : o.note[Tile<BF16, D>::at(r, col >> 2) >> 4];
+        const int col = 32 * b + row_of(i, h);  // 4 neighbouring values of the row
+        if constexpr (BF16) {
+          const uintx2 w = *reinterpret_cast<const uintx2 *>(t + L::at(r, col >> 3) + 2 * (col & 7));
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if ((bits >> e) & 1u) acc[b][i + e] = __builtin_nanf("");
+          for (int e = 0; e < 4; ++e)
+            if (odd(e & 1 ? w[e >> 1] : w[e >> 1] << 16)) acc[b][i + e] = __builtin_nanf("");
+        } else {
+          const uintx4 w = *reinterpret_cast<const uintx4 *>(t + L::at(r, col >> 2));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (odd(w[e])) acc[b][i + e] = __builtin_nanf("");
+        }
       }
 }
 
@@ -311,16 +347,13 @@ __device__ __forceinline__ bool find_block(const int32_t *cu, int B, int T, int 
   return *row0 >= 0;
 }
 
-// Neighbouring workgroups go to the 8 dies in turn; work w = (head, block) runs
-// so that each die takes a contiguous piece, whose heads share keys in its L2.
-// Blocks of a head run longest and shortest in turn, so that pieces are even.
-__device__ __forceinline__ bool find_work(unsigned total, unsigned tiles, unsigned *head, unsigned *tile) {
-  const unsigned per = (total + 7) >> 3, w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || w >= total) return false;
-  *head = w / tiles;
-  const unsigned t = w % tiles;
-  *tile = t & 1 ? t >> 1 : tiles - 1 - (t >> 1);
-  return true;
+// Neighbouring workgroups go to the 8 dies in turn. Blocks run from the one that sees most on, over all heads: the
+// longest first, so that the end is even. Where the heads (of all sequences) divide by 8, a die takes heads that
+// share keys, whose tiles its L2 then holds; otherwise they are dealt out as they come.
+__device__ __forceinline__ void find_work(unsigned units, unsigned *unit, unsigned *rank) {
+  const unsigned i = blockIdx.x % units;
+  *rank = blockIdx.x / units;
+  *unit = units % 8 ? i : (i & 7) * (units >> 3) + (i >> 3);
 }
 
 // A sequence's tokens: the first query and key over the whole batch, how many there are, and
