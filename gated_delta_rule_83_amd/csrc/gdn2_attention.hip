@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   Frag<BF16> q[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
   arrived(q);
-  const float c = p.scale * kLog2e;
+  const Exponent<BF16> power(p.scale);
   // tiles that some query of the workgroup sees; keys that every one of them sees
   const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;  // hi = -1: none
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) t = fmaxf(t, s[u][i]);
-    t = other_half_max(t) * c;
+    t = other_half_max(t) * power.c;
     if (__any(t > top + kSlack)) {
       // each row by its own scores alone, whatever the wave's others do
       const bool grow = t > top + kSlack;
@@ -108,14 +108,15 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
         for (int i = 0; i < 16; ++i) acc[b][i] *= f;
     }
     const float base = top == neg_inf() ? 0.f : top;
+    float own = 0.f;  // this tile's sum
     // Probabilities by groups of 8 registers, each the operand of one step of the
     // second product: the first half of them beside the next scores, each of the
     // others beside the product two (SUB) groups before it.
     auto weigh = [&](int group, int i) __attribute__((always_inline)) {
       floatx16 &x = s[group / 2];
       const int e = 8 * (group % 2) + i;
-      x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], c, -base));
-      sum += x[e];
+      x[e] = __builtin_amdgcn_exp2f(power(x[e], base));
+      own += x[e];
     };
     constexpr int STEPS = D / 16, BLOCKS = D / 32;
     // the SIMD's other wave, in its own turn's vector part, lets the matrix products through
@@ -126,18 +127,29 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
 #pragma unroll
       for (int i = kk * 8 * SUB / STEPS; i < (kk + 1) * 8 * SUB / STEPS; ++i) weigh(i / 8, i % 8);
     }
+    if constexpr (BF16) {
 #pragma unroll
-    for (int g = 0; g < 2 * SUB; ++g) {
-      // bf16: the probabilities' one rounding, 2^-9 of each at most
-      const Frag<BF16> w = operand<BF16>(s[g / 2], g % 2);
+      for (int g = 0; g < 2 * SUB; ++g) {
+        // the probabilities' one rounding, 2^-9 of each at most
+        const Frag<BF16> w = operand<BF16>(s[g / 2], g % 2);
 #pragma unroll
-      for (int b = 0; b < BLOCKS; ++b) {
-        acc[b] = mma<BF16>(acc[b], across.read(vt, 16 * g, b), w);
-        if (g < SUB)
+        for (int b = 0; b < BLOCKS; ++b) {
+          acc[b] = mma<BF16>(acc[b], across.read(vt, 16 * g, b), w);
+          if (g < SUB)
 #pragma unroll
-          for (int i = b * 8 / BLOCKS; i < (b + 1) * 8 / BLOCKS; ++i) weigh(g + SUB, i);
+            for (int i = b * 8 / BLOCKS; i < (b + 1) * 8 / BLOCKS; ++i) weigh(g + SUB, i);
+        }
       }
+    } else {
+      Frag<BF16> w[2 * SUB];
+#pragma unroll
+      for (int i = 8 * SUB; i < 16 * SUB; ++i) weigh(i / 8, i % 8);
+#pragma unroll
+      for (int g = 0; g < 2 * SUB; ++g) w[g] = operand<BF16>(s[g / 2], g % 2);
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) add_products<BF16>(acc[b], [&](int g) { return across.read(vt, 16 * g, b); }, w);
     }
+    sum += own;
     __builtin_amdgcn_s_setprio(0);
   };
 
@@ -192,7 +204,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   const bool empty = hi < lo;  // no key at all: zero, and a log-sum of -inf
   char *out = static_cast<char *>(p.o) + ((sp.q0 + mine) * (int64_t)p.H + head) * D * ES;
   store_row<BF16, D>(out, acc, empty ? 0.f : 1.f / sum, h);
-  if (h == 0 && p.lse) p.lse[sp.rows + mine] = empty ? neg_inf() : __builtin_fmaf(top, kLn2, __logf(sum));
+  if (h == 0 && p.lse) p.lse[sp.rows + mine] = empty ? neg_inf() : __builtin_fmaf(top, kLn2, __builtin_fmaf(top, kLn2Low, __logf(sum)));
 }
 
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {

@@ -5,7 +5,7 @@
 //   dq_i = scale sum_j ds_ij k_j              dk_j = scale sum_i ds_ij q_i
 //
 // Two passes, each of which computes the scores and dp again: one by blocks of
-// queries (dq; it also leaves delta and lse, in powers of two, for the other),
+// queries (dq; it also leaves delta and lse for the other),
 // one by blocks of keys (dk, dv, over the query heads that share them). That is
 // 14 d flops a pair instead of the 10 d of a single pass, whose dq would have to
 // be summed by atomics in an order of their own: here results are the same bits
@@ -17,6 +17,33 @@ namespace gdn2 {
 namespace {
 
 using namespace attn;
+
+// A row's lse in powers of two; in fp32 in two parts, as the factor of its scores.
+template <bool BF16> struct Base {
+  float high, low;
+  Base() = default;
+  __device__ __forceinline__ explicit Base(float lse) {
+    high = lse * kLog2e;
+    low = BF16 || lse == neg_inf() ? 0.f : __builtin_fmaf(lse, kLog2eLow, __builtin_fmaf(lse, kLog2e, -high));
+    pin_regs(high);
+  }
+  // from what the first pass leaves: powers of two in bf16, lse itself in fp32
+  static __device__ __forceinline__ Base at(float left) {
+    Base b;
+    if constexpr (BF16) {
+      b.high = left;
+      b.low = 0.f;
+    } else {
+      b.high = left * kLog2e;
+      b.low = left == neg_inf() ? 0.f : __builtin_fmaf(left, kLog2eLow, __builtin_fmaf(left, kLog2e, -b.high));
+    }
+    return b;
+  }
+  __device__ __forceinline__ float probability(const Exponent<BF16> &power, float s) const {
+    const float x = power(s, high);
+    return __builtin_amdgcn_exp2f(BF16 ? x : x - low);
+  }
+};
 
 // ---------------------------------------------------------------- dq
 template <bool BF16, int D>
@@ -64,13 +91,8 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   }
   arrived(q);
   arrived(g);
-  float lse = p.lse_in[sp.rows + row] * kLog2e;
-  pin_regs(lse);
-  const float c = p.scale * kLog2e;
-  if (mine < m.nq && h == 0) {
-    p.delta[sp.rows + mine] = delta;
-    p.lse[sp.rows + mine] = lse;
-  }
+  const Exponent<BF16> power(p.scale);
+  const Base<BF16> lse(p.lse_in[sp.rows + row]);
   const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;
   const int b_lo = m.lo(blast), b_hi = m.hi(row0);
@@ -86,6 +108,41 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   ks.init(p.sk * ES, tid);
   vs.init(p.sv * ES, tid);
 
+  const int most = m.window ? min(m.window, m.hi(blast) + 1) : m.hi(blast) + 1;  // keys that a query sees at most
+  // delta from o as it was rounded is off by half a step of o, which shows where a query sees few keys and ds is
+  // itself a difference of their size (1024 causal tokens: dq 1.6 times as far off as its own rounding, 1.43 with
+  // the sum in fp32). There delta is summed from the probabilities instead: two products more, for five tiles at most.
+  if (BF16 && t_lo < t_hi && most <= 128) {
+    float own = 0.f;
+#pragma unroll 1
+    for (int t = t_lo; t < t_hi; ++t) {
+      __syncthreads();  // nobody reads the tile before any more
+      ks.load(sm.tile[0][0], kbase, t * KT, m.nk, wave);
+      vs.load(sm.tile[0][1], vbase, t * KT, m.nk, wave);
+      landed();
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        floatx16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          s = mma<BF16>(s, along.read(at, 32 * u, kk), q[kk]);
+          dp = mma<BF16>(dp, along.read(at + TILE, 32 * u, kk), g[kk]);
+        }
+        const int from = lo - t * KT - 4 * h, to = hi - t * KT - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          own += 32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to ? 0.f : lse.probability(power, s[i]) * dp[i];
+      }
+    }
+    __syncthreads();
+    delta = other_half_sum(own);
+  }
+  if (mine < m.nq && h == 0) {
+    p.delta[sp.rows + mine] = delta;
+    p.lse[sp.rows + mine] = BF16 ? lse.high : p.lse_in[sp.rows + mine];
+  }
+
   // ds of 32 keys
   auto part = [&](Frag<BF16> (&ds)[2], uint32_t kt, uint32_t vt, int u, int key0, auto masked) __attribute__((always_inline)) {
     floatx16 s = zero16(), dp = zero16();
@@ -97,7 +154,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
     const int from = lo - key0 - 4 * h, to = hi - key0 - 4 * h;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse)) * (dp[i] - delta);
+      s[i] = lse.probability(power, s[i]) * (dp[i] - delta);
       if constexpr (decltype(masked)::value)
         if (32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to) s[i] = 0.f;
     }
@@ -106,10 +163,17 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
     ds[1] = operand<BF16>(s, 1);
   };
   auto product = [&](const Frag<BF16> (&ds)[2], uint32_t kt, int u) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
+    if constexpr (BF16) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(kt, 32 * u + 16 * e, b), ds[e]);
+        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(kt, 32 * u + 16 * e, b), ds[e]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(kt, 32 * u + 16 * e, b); }, ds);
+    }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   for (bool careful = false;; careful = true) {
@@ -214,7 +278,7 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
   Frag<BF16> kept[D / 16];
   load_row<BF16, D>(kept, static_cast<const char *>(second ? p.v : p.k) + ((sp.k0 + row) * (second ? p.sv : p.sk) + (int64_t)kv * D) * ES, h);
   arrived(kept);
-  const float c = p.scale * kLog2e;
+  const Exponent<BF16> power(p.scale);
   const int first = m.first(row), last = m.last(row);
   // query tiles that some key of the workgroup is seen from; queries that see every one of them
   const int blast = min(row0 + kAttnRows - 1, m.nk - 1);
@@ -258,7 +322,7 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
     for (int i = 0; i < 16; i += 4) {
       const floatx4 l = lds_read<floatx4>(st + 4 * row_of(i, 0));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + e], c, -l[e]));
+      for (int e = 0; e < 4; ++e) s[i + e] = Base<BF16>::at(l[e]).probability(power, s[i + e]);
     }
     if constexpr (decltype(masked)::value) {
 #pragma unroll
@@ -268,12 +332,18 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       *reinterpret_cast<__attribute__((address_space(3))) floatx4 *>((uintptr_t)(pt + i * 256)) = floatx4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};  // bf16: one rounding of each p
+    __builtin_amdgcn_s_setprio(1);
+    if constexpr (BF16) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const Frag<BF16> w = operand<BF16>(s, e);  // bf16: one rounding of each p
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(gt, 16 * e, b), w);
+        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(gt, 16 * e, b), w[e]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(gt, 16 * e, b); }, w);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
   auto slopes = [&](int q0, int buf, auto masked) __attribute__((always_inline)) {
     const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 256 + 16 * h, pt = probs + buf * 4 * PROBS;
@@ -291,12 +361,18 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
       for (int i = 0; i < 16; ++i)
         if (outside(q0, i)) s[i] = 0.f;
     }
+    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};  // bf16: one rounding of each ds
+    __builtin_amdgcn_s_setprio(1);
+    if constexpr (BF16) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const Frag<BF16> w = operand<BF16>(s, e);  // bf16: one rounding of each ds
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(qt, 16 * e, b), w);
+        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(qt, 16 * e, b), w[e]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(qt, 16 * e, b); }, w);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
 
   for (bool careful = false;; careful = true) {

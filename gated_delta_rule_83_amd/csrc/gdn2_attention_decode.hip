@@ -4,7 +4,8 @@
 // The cache is read once, which bounds the call: 2 d values a key and key head,
 // of which 16 query heads' products cost the matrix cores little. A workgroup
 // takes a span of one sequence's keys and one key head, a wave every fourth tile
-// of 32 keys, straight from memory to registers:
+// of 32 keys, straight from memory to registers, the next tile's loads out before
+// this one's are used (N4 131072 tokens: 111 us without, 88 with; 6.2 TB/s):
 //  - scores transposed (keys as rows), 16 x 16: a key's row is an A operand as it
 //    lies, 8 values a lane;
 //  - o transposed, too: row m of block r is channel m D / 16 + r, so a lane's
@@ -41,19 +42,24 @@ template <bool BF16> __device__ __forceinline__ floatx4 mma16(floatx4 acc, const
   }
 }
 
+// Cache rows are read once: nontemporal where a load takes whole lines.
+template <class V> __device__ __forceinline__ V load_once(const char *p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
+}
+
 // 8 keys' pieces of D / 16 channels.
 template <bool BF16, int D> struct Values {
   static constexpr int C = D / 16, W = BF16 ? C / 2 : C;  // channels and words of a piece
   uint32_t w[8][W];
   __device__ __forceinline__ void load(int j, const char *p) {
     if constexpr (W == 2) {
-      const uintx2 x = *reinterpret_cast<const uintx2 *>(p);
+      const uintx2 x = load_once<uintx2>(p);
       w[j][0] = x[0];
       w[j][1] = x[1];
     } else {
 #pragma unroll
       for (int i = 0; i < W; i += 4) {
-        const uintx4 x = *reinterpret_cast<const uintx4 *>(p + 4 * i);
+        const uintx4 x = load_once<uintx4>(p + 4 * i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[j][i + e] = x[e];
       }
@@ -92,7 +98,7 @@ __device__ __forceinline__ int first_key(const DecodeArgs &p, int len) {
 
 // ONE: a tile of 32 keys lies in one page.
 template <bool BF16, int D, bool ONE>
-__global__ void __launch_bounds__(256, 2) attention_decode_kernel(const DecodeArgs p, const DecodePlan plan, int shift) {
+__global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_decode_kernel(const DecodeArgs p, const DecodePlan plan, int shift) {
   using Vals = Values<BF16, D>;
   constexpr int ES = BF16 ? 2 : 4, C = Vals::C;
   __shared__ float part_o[kWaves][16][D + 4];
@@ -127,15 +133,18 @@ __global__ void __launch_bounds__(256, 2) attention_decode_kernel(const DecodeAr
   // the row of key `key` of page `page` in the cache, in values
   auto row_at = [&](int page, int key) { return (((int64_t)page * p.Hkv + kv) * p.page + (key & (p.page - 1))) * D; };
 
-  floatx4 acc[C];
-#pragma unroll
-  for (int r = 0; r < C; ++r) acc[r] = zero4();
-  float top = neg_inf(), sum = 0.f;
-  for (int key0 = begin + kTileKeys * wave; key0 < end; key0 += kTileKeys * kWaves) {
+  // One tile on its way: keys as score operands, values, whether the keys of this lane's 8 slots are seen.
+  struct Load {
+    Frag<BF16> k[2][D / 32];
+    Vals v;
+    uint32_t seen;
+  };
+  // ONE: the page of the tile; else pages are looked up key by key
+  auto page_of = [&](int key0) { return ONE && key0 < end ? table[__builtin_amdgcn_readfirstlane(key0 >> shift)] : -1; };
+  auto load = [&](Load &x, int key0, int page) __attribute__((always_inline)) {
     int64_t kat[2], vat[8];
-    uint32_t vok = 0;  // whether the keys of this lane's 8 slots are seen
+    x.seen = 0;
     if constexpr (ONE) {
-      const int page = table[__builtin_amdgcn_readfirstlane(key0 >> shift)];
       const bool there = page >= 0 && page < p.P;
       const int64_t base = row_at(there ? page : 0, key0);
 #pragma unroll
@@ -144,52 +153,56 @@ __global__ void __launch_bounds__(256, 2) attention_decode_kernel(const DecodeAr
       for (int j = 0; j < 8; ++j) {
         const int key = 16 * (j >> 2) + 4 * g + (j & 3);
         vat[j] = base + key * D;
-        vok |= (uint32_t)(there && key0 + key >= lo && key0 + key < end) << j;
+        x.seen |= (uint32_t)(there && key0 + key >= lo && key0 + key < end) << j;
       }
     } else {
       const int most = p.M - 1;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int key = key0 + 16 * u + col, page = table[min(key >> shift, most)];
-        kat[u] = row_at(page >= 0 && page < p.P ? page : 0, key);
+        const int key = key0 + 16 * u + col, pg = table[min(key >> shift, most)];
+        kat[u] = row_at(pg >= 0 && pg < p.P ? pg : 0, key);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3), page = table[min(key >> shift, most)];
-        const bool there = page >= 0 && page < p.P;
-        vat[j] = row_at(there ? page : 0, key);
-        vok |= (uint32_t)(there && key >= lo && key < end) << j;
+        const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3), pg = table[min(key >> shift, most)];
+        const bool there = pg >= 0 && pg < p.P;
+        vat[j] = row_at(there ? pg : 0, key);
+        x.seen |= (uint32_t)(there && key >= lo && key < end) << j;
       }
     }
-    Frag<BF16> k[2][D / 32];
-    Vals v;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) {
         const char *src = kc + (kat[u] + 32 * kk + 8 * g) * ES;
         if constexpr (BF16) {
-          k[u][kk].v = *reinterpret_cast<const bf16x8 *>(src);
+          x.k[u][kk].v = *reinterpret_cast<const bf16x8 *>(src);
         } else {
           const floatx4 *f = reinterpret_cast<const floatx4 *>(src);
-          k[u][kk].v = __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7);
+          x.k[u][kk].v = __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7);
         }
       }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v.load(j, vc + (vat[j] + col * C) * ES);
+    for (int j = 0; j < 8; ++j) x.v.load(j, vc + (vat[j] + col * C) * ES);
+  };
+
+  floatx4 acc[C];
+#pragma unroll
+  for (int r = 0; r < C; ++r) acc[r] = zero4();
+  float top = neg_inf(), sum = 0.f;
+  auto take = [&](Load &x) __attribute__((always_inline)) {
     floatx4 s[2] = {zero4(), zero4()};
 #pragma unroll
     for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) s[u] = mma16<BF16>(s[u], k[u][kk], q[kk]);
+      for (int u = 0; u < 2; ++u) s[u] = mma16<BF16>(s[u], x.k[u][kk], q[kk]);
     // a lane's scores are of the keys of its 8 slots
-    const bool all = __all(vok == 0xffu);
-    if (!all) {
+    if (!__all(x.seen == 0xffu)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (!((vok >> j) & 1u)) {
+        if (!((x.seen >> j) & 1u)) {
           s[j >> 2][j & 3] = neg_inf();
-          v.zero(j);  // whatever lies behind the last key
+          x.v.zero(j);  // whatever lies behind the last key
         }
     }
     float t = neg_inf();
@@ -215,7 +228,28 @@ __global__ void __launch_bounds__(256, 2) attention_decode_kernel(const DecodeAr
     if constexpr (BF16) pw.v = __builtin_convertvector(w, bf16x8);  // the probabilities' one rounding
     else pw.v = w;
 #pragma unroll
-    for (int r = 0; r < C; ++r) acc[r] = mma16<BF16>(acc[r], v.block(r), pw);
+    for (int r = 0; r < C; ++r) acc[r] = mma16<BF16>(acc[r], x.v.block(r), pw);
+  };
+
+  // the next tile's loads are out before this one's are waited for, its page one tile earlier
+  constexpr int STEP = kTileKeys * kWaves;
+  int key0 = begin + kTileKeys * wave;
+  if (key0 < end) {
+    Load x[2];
+    int page = page_of(key0), next = page_of(key0 + STEP);
+    load(x[0], key0, page);
+    for (;; key0 += 2 * STEP) {
+      page = next;
+      next = page_of(key0 + 2 * STEP);
+      if (key0 + STEP < end) load(x[1], key0 + STEP, page);
+      take(x[0]);
+      if (key0 + STEP >= end) break;
+      page = next;
+      next = page_of(key0 + 3 * STEP);
+      if (key0 + 2 * STEP < end) load(x[0], key0 + 2 * STEP, page);
+      take(x[1]);
+      if (key0 + 2 * STEP >= end) break;
+    }
   }
   sum = column_sum(sum);
 
@@ -262,38 +296,44 @@ __global__ void __launch_bounds__(256, 2) attention_decode_kernel(const DecodeAr
   }
 }
 
-// One workgroup a query head: its spans' sums, a wave every fourth of them, D / 64 channels a lane.
-template <bool BF16, int D> __global__ void __launch_bounds__(256) attention_decode_join_kernel(const DecodeArgs p, const DecodePlan plan) {
+// One workgroup a query head: its spans' sums, dealt out to WAVES waves, D / 64 neighbouring channels a lane.
+template <bool BF16, int D, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) attention_decode_join_kernel(const DecodeArgs p, const DecodePlan plan) {
   constexpr int V = D / 64;
-  __shared__ float sums[kWaves][D + 1];
+  __shared__ float sums[WAVES][D + 1];
   const int64_t at = blockIdx.x;
   const int n = (int)(at / p.H), len = length_of(p, n), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // span 0 is always written
   const int live = max(1, (len - first_key(p, len) + plan.span - 1) / plan.span);
   const float *ml = p.workspace + at * plan.splits * 2;
-  const float *os = p.workspace + (int64_t)p.N * p.H * plan.splits * 2 + at * plan.splits * D;
+  const float *os = p.workspace + (int64_t)p.N * p.H * plan.splits * 2 + at * plan.splits * D + V * lane;
   float most = neg_inf();
   for (int s = lane; s < live; s += 64) most = fmaxf(most, ml[2 * s]);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
   float o[V] = {}, l = 0.f;
 #pragma unroll 4
-  for (int s = wave; s < live; s += kWaves) {
+  for (int s = wave; s < live; s += WAVES) {
     const float f = ml[2 * s] == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(ml[2 * s] - most);
     l += f * ml[2 * s + 1];
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] += f * os[(int64_t)s * D + lane + 64 * e];
+    for (int e = 0; e < V; ++e) o[e] += f * os[(int64_t)s * D + e];
   }
 #pragma unroll
-  for (int e = 0; e < V; ++e) sums[wave][lane + 64 * e] = o[e];
+  for (int e = 0; e < V; ++e) sums[wave][V * lane + e] = o[e];
   if (lane == 0) sums[wave][D] = l;
   __syncthreads();
-  l = sums[0][D] + sums[1][D] + sums[2][D] + sums[3][D];
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int d = threadIdx.x; d < D; d += 256) {
-    const float y[1] = {(sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d]) * inv};
-    store_f<BF16, 1>(p.o, (size_t)(at * D + d), y);
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  l = 0.f;
+  float y[1] = {0.f};
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    l += sums[w][D];
+    y[0] += sums[w][d];
   }
+  y[0] *= l == 0.f ? 0.f : 1.f / l;
+  store_f<BF16, 1>(p.o, (size_t)(at * D + d), y);
 }
 
 // ---------------------------------------------------------------- the cache's writes
@@ -341,14 +381,19 @@ template <bool BF16, int D> hipError_t run(const DecodeArgs &p, const DecodePlan
   if (p.page >= kTileKeys) attention_decode_kernel<BF16, D, true><<<grid, 256, 0, stream>>>(p, plan, shift);
   else attention_decode_kernel<BF16, D, false><<<grid, 256, 0, stream>>>(p, plan, shift);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess || plan.splits == 1) return e;
-  attention_decode_join_kernel<BF16, D><<<(unsigned)((size_t)p.N * p.H), 256, 0, stream>>>(p, plan);
+  // few heads over many spans: 16 waves a head (N4 H16, 256 spans: 86 us in all against 88); many heads over few
+  // spans: 4 (N256 H16, 4 spans: 208 against 220)
+  const unsigned heads = (unsigned)((size_t)p.N * p.H);
+  if (plan.splits > 32) attention_decode_join_kernel<BF16, D, 16><<<heads, 1024, 0, stream>>>(p, plan);
+  else attention_decode_join_kernel<BF16, D, 4><<<heads, 256, 0, stream>>>(p, plan);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // A span is as long as leaves 2048 workgroups, 8 a CU, which even out sequences
-// of different lengths; 128 keys (a tile a wave) at least.
+// of different lengths (N256 up to 8192 tokens H16/2 d128 bf16: 208 us, 216 with
+// 1024, 214 with 4096); 128 keys (a tile a wave) at least.
 DecodePlan decode_plan(int N, int H, int Hkv, int M, int page, int window) {
   const int64_t all = (int64_t)M * page;
   // a window's keys begin inside a tile

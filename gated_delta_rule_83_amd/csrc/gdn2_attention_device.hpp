@@ -27,10 +27,25 @@ typedef float floatx8 __attribute__((ext_vector_type(8)));
 typedef short shortx8 __attribute__((ext_vector_type(8)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
-constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = (float)(1.44269504088896341 - (double)kLog2e);
+constexpr float kLn2 = 0.693147180559945309f, kLn2Low = (float)(0.693147180559945309 - (double)kLn2);
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// Exponents of 2 for scale * s - base. In fp32 the factor scale * log2 e is kept
+// in two parts: its rounding alone would show in every probability.
+template <bool BF16> struct Exponent {
+  float c, low;
+  __device__ __forceinline__ explicit Exponent(float scale) {
+    c = scale * kLog2e;
+    low = BF16 ? 0.f : __builtin_fmaf(scale, kLog2eLow, __builtin_fmaf(scale, kLog2e, -c));
+  }
+  // base in powers of two
+  __device__ __forceinline__ float operator()(float s, float base) const {
+    const float x = __builtin_fmaf(s, c, -base);
+    return BF16 || s == neg_inf() ? x : __builtin_fmaf(s, low, x);
+  }
+};
 
 template <bool BF16> struct Frag;
 template <> struct Frag<true> { bf16x8 v; };
@@ -61,6 +76,16 @@ template <bool BF16> __device__ __forceinline__ Frag<BF16> operand(const floatx1
   for (int j = 0; j < 8; ++j) y[j] = x[8 * s + j];
   if constexpr (BF16) return Frag<true>{__builtin_convertvector(y, bf16x8)};
   else return Frag<false>{y};
+}
+
+// acc += sum of N operands' products. In fp32 the sum of a tile is one of its
+// own first: a chain over all of a long sequence would lose half a digit.
+template <bool BF16, int N, class A> __device__ __forceinline__ void add_products(floatx16 &acc, A a, const Frag<BF16> (&b)[N]) {
+  floatx16 t = BF16 ? acc : zero16();
+#pragma unroll
+  for (int i = 0; i < N; ++i) t = mma<BF16>(t, a(i), b[i]);
+  if constexpr (BF16) acc = t;
+  else acc += t;
 }
 
 // row of register i of a lane of half h
