@@ -11,6 +11,14 @@
 // be summed by atomics in an order of their own: here results are the same bits
 // at every run. Scores are kept so that the rows of the product to come are the
 // registers: keys for dq, queries for dk and dv.
+//
+// bf16 operands of the last products: p and ds are rounded once, 2^-9 at most,
+// which is the size of the results' own rounding. In tiles of which some places
+// are hidden (the diagonal's: there rows see few keys, and the largest
+// probabilities are) the remainder goes through the product as well: gradients
+// of 4096 causal tokens are 1.25 times as far off as their own rounding, of 200
+// tokens 1.06 times, where one operand leaves 1.45 and 1.47; it costs 2% (B4
+// T4096 H16/2 d128: 984 -> 1005 us).
 #include "gdn2_attention_device.hpp"
 
 namespace gdn2 {
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   }
 
   // ds of 32 keys
-  auto part = [&](Frag<BF16> (&ds)[2], uint32_t kt, uint32_t vt, int u, int key0, auto masked) __attribute__((always_inline)) {
+  auto part = [&](Frag<BF16> (&ds)[2], Frag<BF16> (&rest)[2], uint32_t kt, uint32_t vt, int u, int key0, auto masked) __attribute__((always_inline)) {
     floatx16 s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -158,17 +166,23 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
       if constexpr (decltype(masked)::value)
         if (32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to) s[i] = 0.f;
     }
-    // bf16: one rounding of each ds
-    ds[0] = operand<BF16>(s, 0);
-    ds[1] = operand<BF16>(s, 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ds[e] = operand<BF16>(s, e);
+      if constexpr (BF16 && decltype(masked)::value) rest[e] = remainder<BF16>(s, e, ds[e]);
+    }
   };
-  auto product = [&](const Frag<BF16> (&ds)[2], uint32_t kt, int u) __attribute__((always_inline)) {
+  auto product = [&](const Frag<BF16> (&ds)[2], const Frag<BF16> (&rest)[2], uint32_t kt, int u, auto masked) __attribute__((always_inline)) {
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BF16) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(kt, 32 * u + 16 * e, b), ds[e]);
+        for (int b = 0; b < D / 32; ++b) {
+          const Frag<BF16> x = across.read(kt, 32 * u + 16 * e, b);
+          acc[b] = mma<BF16>(acc[b], x, ds[e]);
+          if constexpr (decltype(masked)::value) acc[b] = mma<BF16>(acc[b], x, rest[e]);
+        }
     } else {
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(kt, 32 * u + 16 * e, b); }, ds);
@@ -192,23 +206,23 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
         vs.load(sm.tile[BUF ^ 1][1], vbase, key0 + KT, m.nk, wave);
       }
       const uint32_t kt = at + 2 * BUF * TILE, vt = kt + TILE;
-      Frag<BF16> ds[SUB][2];
+      Frag<BF16> ds[SUB][2], rest[SUB][2];
       if (hides(key0)) {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) part(ds[u], kt, vt, u, key0, std::true_type{});
+        for (int u = 0; u < SUB; ++u) part(ds[u], rest[u], kt, vt, u, key0, std::true_type{});
         if (careful) {  // the scores take K as it is, the product without its odd values
           __syncthreads();
           clean<BF16, TILE>(sm.tile[BUF][0], tid);
         }
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) product(ds[u], kt, u);
+        for (int u = 0; u < SUB; ++u) product(ds[u], rest[u], kt, u, std::true_type{});
       } else {
         // each 32 keys' product beside the next ones' scores
-        part(ds[0], kt, vt, 0, key0, std::false_type{});
+        part(ds[0], rest[0], kt, vt, 0, key0, std::false_type{});
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          if (u + 1 < SUB) part(ds[u + 1], kt, vt, u + 1, key0, std::false_type{});
-          product(ds[u], kt, u);
+          if (u + 1 < SUB) part(ds[u + 1], rest[u + 1], kt, vt, u + 1, key0, std::false_type{});
+          product(ds[u], rest[u], kt, u, std::false_type{});
         }
       }
     };
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
 // stand beside the one of ds). So both have two products a tile and registers
 // for two waves a SIMD, one of each kind; with all four products and both
 // accumulators in one wave there is one a SIMD, whose vector instructions keep
-// the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us).
+// the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us, so 665).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
@@ -332,13 +346,20 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
 #pragma unroll
     for (int i = 0; i < 16; i += 4)
       *reinterpret_cast<__attribute__((address_space(3))) floatx4 *>((uintptr_t)(pt + i * 256)) = floatx4{s[i], s[i + 1], s[i + 2], s[i + 3]};
-    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};  // bf16: one rounding of each p
+    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BF16) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        Frag<BF16> rest;
+        if constexpr (decltype(masked)::value) rest = remainder<BF16>(s, e, w[e]);
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(gt, 16 * e, b), w[e]);
+        for (int b = 0; b < D / 32; ++b) {
+          const Frag<BF16> x = across.read(gt, 16 * e, b);
+          acc[b] = mma<BF16>(acc[b], x, w[e]);
+          if constexpr (decltype(masked)::value) acc[b] = mma<BF16>(acc[b], x, rest);
+        }
+      }
     } else {
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(gt, 16 * e, b); }, w);
@@ -361,13 +382,20 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
       for (int i = 0; i < 16; ++i)
         if (outside(q0, i)) s[i] = 0.f;
     }
-    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};  // bf16: one rounding of each ds
+    const Frag<BF16> w[2] = {operand<BF16>(s, 0), operand<BF16>(s, 1)};
     __builtin_amdgcn_s_setprio(1);
     if constexpr (BF16) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        Frag<BF16> rest;
+        if constexpr (decltype(masked)::value) rest = remainder<BF16>(s, e, w[e]);
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) acc[b] = mma<BF16>(acc[b], across.read(qt, 16 * e, b), w[e]);
+        for (int b = 0; b < D / 32; ++b) {
+          const Frag<BF16> x = across.read(qt, 16 * e, b);
+          acc[b] = mma<BF16>(acc[b], x, w[e]);
+          if constexpr (decltype(masked)::value) acc[b] = mma<BF16>(acc[b], x, rest);
+        }
+      }
     } else {
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) add_products<BF16>(acc[b], [&](int e) { return across.read(qt, 16 * e, b); }, w);

@@ -78,6 +78,14 @@ template <bool BF16> __device__ __forceinline__ Frag<BF16> operand(const floatx1
   else return Frag<false>{y};
 }
 
+// what an operand's rounding left of x
+template <bool BF16> __device__ __forceinline__ Frag<BF16> remainder(const floatx16 &x, int s, const Frag<BF16> &w) {
+  floatx16 y;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = x[8 * s + j] - (float)w.v[j];
+  return operand<BF16>(y, 0);
+}
+
 // acc += sum of N operands' products. In fp32 the sum of a tile is one of its
 // own first: a chain over all of a long sequence would lose half a digit.
 template <bool BF16, int N, class A> __device__ __forceinline__ void add_products(floatx16 &acc, A a, const Frag<BF16> (&b)[N]) {
