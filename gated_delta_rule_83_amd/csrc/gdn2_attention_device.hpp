@@ -118,20 +118,29 @@ template <class V> __device__ __forceinline__ V lds_read(uint32_t at) {
 
 // A lane's places in a tile. Rows 16 apart are exchanged alike, so the places of
 // rows r .. r + 15 serve all the others: what a read adds is a constant.
-template <bool BF16, int D> struct Along {  // rows as rows or columns of an operand, contracted along them
+// LEAN (fp32): addresses are computed at every read; kept over a loop, as the compiler would, they take 2 registers a
+// step and 8 a block.
+template <bool BF16, int D, bool LEAN = false> struct Along {  // rows as rows or columns of an operand, contracted along them
   using L = Tile<BF16, D>;
-  uint32_t off[D / 16];
+  uint32_t off[BF16 ? D / 16 : 1];
   __device__ __forceinline__ void init(int lane) {
     const int r = lane & 31, h = lane >> 5;
+    if constexpr (BF16) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) off[kk] = L::at(r, BF16 ? 2 * kk + h : 4 * kk + 2 * h);
+      for (int kk = 0; kk < D / 16; ++kk) off[kk] = L::at(r, 2 * kk + h);
+    } else {
+      off[0] = L::at(r, 2 * h);  // step kk: chunk 4 kk on top, in bits of its own
+    }
   }
   // row r0 + (lane & 31), values 16 kk + 8 h ..; tile: LDS address; r0 a multiple of 16
   __device__ __forceinline__ Frag<BF16> read(uint32_t tile, int r0, int kk) const {
     if constexpr (BF16) {
       return Frag<true>{lds_read<bf16x8>(off[kk] + (tile + r0 * L::ROW))};
     } else {
-      const floatx4 x = lds_read<floatx4>(off[kk] + (tile + r0 * L::ROW)), y = lds_read<floatx4>((off[kk] ^ 16) + (tile + r0 * L::ROW));
+      uint32_t o = off[0];
+      if constexpr (LEAN) pin_regs(o);
+      o ^= (uint32_t)(4 * kk) << 4;
+      const floatx4 x = lds_read<floatx4>(o + (tile + r0 * L::ROW)), y = lds_read<floatx4>((o ^ 16) + (tile + r0 * L::ROW));
       return Frag<false>{__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)};
     }
   }
@@ -141,7 +150,7 @@ template <bool BF16, int D> struct Along {  // rows as rows or columns of an ope
 // bf16: in a transposing read lane 4 a + b of 16 receives value b of the 8 bytes
 // that lanes a, a + 4, a + 8 and a + 12 address, so lane j addresses row j / 4,
 // columns 4 (j % 4).
-template <bool BF16, int D> struct Across {
+template <bool BF16, int D, bool LEAN = false> struct Across {
   using L = Tile<BF16, D>;
   uint32_t off[D / 32][BF16 ? 2 : 1];
   __device__ __forceinline__ void init(int lane) {
@@ -169,11 +178,13 @@ template <bool BF16, int D> struct Across {
       return Frag<true>{__builtin_shufflevector(rd(off[b][0]), rd(off[b][1]), 0, 1, 2, 3, 4, 5, 6, 7)};
     } else {
       Frag<false> f;
+      uint32_t x = off[b][0];
+      if constexpr (LEAN) pin_regs(x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         constexpr int ROW = L::ROW;
         const int r = 8 * (j >> 2) + (j & 3);  // on top of 4 h: bits of their own, in the exchange too
-        f.v[j] = lds_read<float>((off[b][0] ^ (L::swizzle(r) << 4)) + (at + r * ROW));
+        f.v[j] = lds_read<float>((x ^ (L::swizzle(r) << 4)) + (at + r * ROW));
       }
       return f;
     }
