@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4;  // 16 KB a tile of K or V at D = 128
   constexpr int TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
-    char tile[2][2][TILE];  // first: within the 64 KB that m0 addresses
+    char tile[2][2][TILE];
     uint32_t said[4];
   } sm;
   unsigned unit, rank;

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   using L = Tile<BF16, D>;
   constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4, TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
-    char tile[2][2][TILE];  // first: within the 64 KB that m0 addresses
+    char tile[2][2][TILE];
     uint32_t said[4];
   } sm;
   unsigned unit, rank;
