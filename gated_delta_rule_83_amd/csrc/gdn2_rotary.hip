@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) rotary_forward_kernel(const RotaryArgs p,
 // The weights' sums stay in registers over all of a wave's rows; then one row
 // of [2][d] a workgroup, which the next kernel adds up in a fixed order.
 template <class P, bool BF16, bool WBF16, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) rotary_backward_kernel(const RotaryArgs p, int pieces, int heads) {
+__global__ void __launch_bounds__(256, P::WIDE ? 5 : 2) rotary_backward_kernel(const RotaryArgs p, int pieces, int heads) {
   using R = Row<P, BF16, NEIGHBOURS>;
   constexpr int ES = BF16 ? 2 : 4;
   __shared__ float share[P::WIDE ? kWaves : 1][256];
@@ -313,7 +313,10 @@ Grid grid_of(int64_t tokens, int all, int rows, unsigned most) {
   return g;
 }
 
-constexpr unsigned kForwardGroups = 2048, kBackwardGroups = 1024;
+// Forward: more workgroups than fit, so that the card's dies end together (32768 tokens H16/2 d128 bf16: 56 us, 65 with
+// 2048). Backward: as many as fit, 5 a CU by its registers, whose weights' sums are one row each (102 us; 113 with
+// 1024, 119 with 2048).
+constexpr unsigned kForwardGroups = 8192, kBackwardGroups = 1280;
 
 bool wide(const RotaryArgs &p, bool backward) {
   const uintptr_t es = p.bf16 ? 2 : 4, ws = p.wbf16 ? 2 : 4;
