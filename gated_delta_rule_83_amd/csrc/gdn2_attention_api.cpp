@@ -68,7 +68,7 @@ gdn2::RotaryArgs rotary_args(const gdn2_rotary_desc *d, const void *q, const voi
 }
 
 // ------------------------------------------------------------------ attention
-gdn2_status check_attention(const gdn2_attention_desc *d, bool packed) {
+gdn2_status check_attention(const gdn2_attention_desc *d, bool packed, bool backward) {
   if (!d) return GDN2_ERR_NULL_POINTER;
   if (!known(d->dtype)) return GDN2_ERR_BAD_DTYPE;
   if (d->B < 0 || d->T_q < 0 || d->T_k < 0 || d->H < 1 || d->H_kv < 1 || d->H % d->H_kv || d->window < 0 || !(d->scale > 0.f) ||
@@ -82,13 +82,13 @@ gdn2_status check_attention(const gdn2_attention_desc *d, bool packed) {
   const size_t es = size_of(d->dtype);
   if (d->stride_q * es % 16 || d->stride_k * es % 16 || d->stride_v * es % 16) return GDN2_ERR_BAD_SHAPE;
   if (d->T_q > INT32_MAX - 256 || d->T_k > INT32_MAX - 256) return GDN2_ERR_UNSUPPORTED;
-  // workgroups: blocks of 128 rows, and a head each
+  // workgroups: blocks of 128 rows, and a head each; 512 threads in the backward
+  const size_t most = backward ? kMaxGroups / 2 : kMaxGroups, B = (size_t)d->B;
   for (const int T : {d->T_q, d->T_k}) {
-    const size_t blocks = packed ? (size_t)T / gdn2::kAttnRows + (size_t)d->B : ceil_div((size_t)T, gdn2::kAttnRows);
-    if (blocks > kMaxGroups || blocks * (size_t)d->H > kMaxGroups || (!packed && blocks * (size_t)d->H * (size_t)d->B > kMaxGroups))
+    const size_t blocks = packed ? (size_t)T / gdn2::kAttnRows + B : ceil_div((size_t)T, gdn2::kAttnRows);
+    if (blocks > most || B > most || blocks * (size_t)d->H > most || (!packed && blocks * (size_t)d->H * B > most))
       return GDN2_ERR_UNSUPPORTED;
   }
-  if ((size_t)d->B > kMaxGroups) return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;
 }
 
@@ -110,7 +110,7 @@ gdn2::AttentionArgs attention_args(const gdn2_attention_desc *d) {
 
 gdn2_status attention_forward(const gdn2_attention_desc *d, bool packed, const int32_t *cu_q, const int32_t *cu_k, const void *q,
                               const void *k, const void *v, void *o, float *lse, void *stream) {
-  const gdn2_status st = check_attention(d, packed);
+  const gdn2_status st = check_attention(d, packed, false);
   if (st != GDN2_OK) return st;
   const int64_t nq = q_rows(d, packed), nk = k_rows(d, packed);
   if (d->B == 0 || nq == 0) return GDN2_OK;
@@ -145,13 +145,13 @@ BackwardSpace backward_space(const gdn2_attention_desc *d, bool packed) {
   return s;
 }
 size_t attention_backward_ws(const gdn2_attention_desc *d, bool packed) {
-  return check_attention(d, packed) != GDN2_OK || d->B == 0 ? 0 : backward_space(d, packed).bytes;
+  return check_attention(d, packed, true) != GDN2_OK || d->B == 0 ? 0 : backward_space(d, packed).bytes;
 }
 
 gdn2_status attention_backward(const gdn2_attention_desc *d, bool packed, const int32_t *cu_q, const int32_t *cu_k, const void *q,
                                const void *k, const void *v, const void *o, const float *lse, const void *dO, void *dq, void *dk,
                                void *dv, void *workspace, size_t workspace_bytes, void *stream) {
-  const gdn2_status st = check_attention(d, packed);
+  const gdn2_status st = check_attention(d, packed, true);
   if (st != GDN2_OK) return st;
   const int64_t nq = q_rows(d, packed), nk = k_rows(d, packed);
   if (nq == 0 && nk == 0) return GDN2_OK;
@@ -198,7 +198,8 @@ gdn2_status check_decode(const gdn2_attention_decode_desc *d) {
   if ((d->d != 64 && d->d != 128) || !power_of_two(d->page) || (int64_t)d->M * d->page > 1 << 30) return GDN2_ERR_UNSUPPORTED;
   const gdn2::DecodePlan plan = gdn2::decode_plan(d->N, d->H, d->H_kv, d->M, d->page, d->window);
   const size_t heads = (size_t)d->N * d->H;
-  if (heads > kMaxGroups || (size_t)d->N * d->H_kv * plan.tiles * plan.splits > kMaxGroups) return GDN2_ERR_UNSUPPORTED;
+  // a join of 1024 threads a head
+  if (heads > kMaxGroups / 4 || (size_t)d->N * d->H_kv * plan.tiles * plan.splits > kMaxGroups) return GDN2_ERR_UNSUPPORTED;
   return GDN2_OK;
 }
 

@@ -489,20 +489,17 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
   }
 }
 
-// Sums of the parts, in order; four values a thread. Rows of no sequence are left to the next kernel.
+// Sums of the parts, in order; four values a thread. Rows of no sequence: see the next kernel.
 template <bool BF16> __global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs p, int64_t n) {
-  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x), w = (int64_t)p.Hkv * p.d;
-  if (i >= n) return;
-  if (p.cu_q) {
-    const int64_t token = i / w;
-    if (token < clamp_to(p.cu_k[0], p.Tk) || token >= clamp_to(p.cu_k[p.B], p.Tk)) return;
-  }
-  for (int out = 0; out < 2; ++out) {
-    floatx4 x = *reinterpret_cast<const floatx4 *>(p.partial + out * n + i);
-    for (int k = 1; k < p.parts; ++k) x += *reinterpret_cast<const floatx4 *>(p.partial + (2 * k + out) * n + i);
-    const float y[4] = {x[0], x[1], x[2], x[3]};
-    store_f<BF16, 4>(out ? p.dv : p.dk, (size_t)i, y);
-  }
+  const int64_t w = (int64_t)p.Hkv * p.d, from = p.cu_q ? clamp_to(p.cu_k[0], p.Tk) * w : 0;
+  const int64_t to = p.cu_q ? clamp_to(p.cu_k[p.B], p.Tk) * w : n;
+  for (int64_t i = from + 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < to; i += 1024 * (int64_t)gridDim.x)
+    for (int out = 0; out < 2; ++out) {
+      floatx4 x = *reinterpret_cast<const floatx4 *>(p.partial + out * n + i);
+      for (int k = 1; k < p.parts; ++k) x += *reinterpret_cast<const floatx4 *>(p.partial + (2 * k + out) * n + i);
+      const float y[4] = {x[0], x[1], x[2], x[3]};
+      store_f<BF16, 4>(out ? p.dv : p.dk, (size_t)i, y);
+    }
 }
 
 // Gradients of packed tokens of no sequence: zero. One workgroup row by row of the tokens before the first and
@@ -540,7 +537,8 @@ template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t s
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (p.parts > 1) {
     const int64_t n = (int64_t)seqs * p.Tk * p.Hkv * D;
-    attention_join_kernel<BF16><<<(unsigned)((n / 4 + 255) / 256), 256, 0, stream>>>(p, n);
+    const int64_t groups = (n / 4 + 255) / 256;
+    attention_join_kernel<BF16><<<(unsigned)(groups < 65536 ? groups : 65536), 256, 0, stream>>>(p, n);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   return hipSuccess;

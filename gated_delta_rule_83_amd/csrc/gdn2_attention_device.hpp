@@ -204,14 +204,16 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__bui
 template <int BYTES> __device__ __forceinline__ void dma(const char *base, uint32_t bytes, uint32_t off, uint32_t to) {
   const uintx4 rsrc = {uniform((uint32_t)(uintptr_t)base), uniform((uint32_t)((uintptr_t)base >> 32)) & 0xffffu, uniform(bytes),
                        0x00020000u};
-  // nothing else in these kernels uses m0; the nop is the wait between its write and its use
+  // Nothing else in these kernels uses m0. The compiler knows of no hazard inside the asm: one wait state between the
+  // write of m0 and its use, five between a vector instruction's write of a scalar register (the descriptor's, by
+  // readfirstlane) and a memory instruction's read of it.
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(uniform(to)), "v"(off), "s"(rsrc)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(uniform(to)), "v"(off), "s"(rsrc)
                  : "memory");

@@ -694,7 +694,8 @@ gdn2_status gdn2_rotary_backward(const gdn2_rotary_desc *desc, const void *q, co
  *   q : [B, T_q, H, d]   k, v : [B, T_k, H_kv, d]   o : [B, T_q, H, d]   in dtype
  *   lse : [B, H, T_q] fp32, may be NULL in the forward
  * d 64 or 128 (GDN2_ERR_UNSUPPORTED otherwise); scale > 0, finite; any B, T >= 0 with
- * B * H * ceil(T / 128) <= 2^24 - 1 (both T), T <= 2^31 - 257; H * d and strides up to 2^22.
+ * B * H * ceil(T / 128) <= 2^24 - 1 (both T; half of that in the backward), T <= 2^31 - 257; H * d and strides up
+ * to 2^22.
  * Tensors and strides are 16-byte aligned, lse and offsets 4-byte.
  * Scores, sums and softmax are fp32; with bf16 inputs the probabilities (and
  * their gradients) are rounded to bf16 once as operands of the matrix products,
@@ -745,7 +746,7 @@ gdn2_status gdn2_attention_backward_varlen(const gdn2_attention_desc *desc, cons
  * in the cache), sees all of them or (window > 0) the last `window`. Tokens of a
  * page outside [0, P) are not seen; whatever a page holds behind a sequence's last
  * token is not read into any result. A query that sees no token (or scores of -inf alone) gives zeros.
- *   q, o : [N, H, d]    d 64 or 128; H % H_kv == 0; N * H and the call's workgroups up to 2^24 - 1
+ *   q, o : [N, H, d]    d 64 or 128; H % H_kv == 0; N * H up to 2^22 - 1, the call's workgroups up to 2^24 - 1
  * The work is split over the longest length that the table has room for; the
  * spans' partial results (fp32) lie in the workspace
  * (gdn2_attention_decode_workspace_bytes(desc) bytes, 16-byte aligned). */

@@ -100,6 +100,9 @@ def test_attention_limits_count_blocks():
     for T in (dict(T_q=2 ** 31 - 257, T_k=1), dict(T_k=2 ** 31 - 257, T_q=1)):
         assert g.gdn2_attention_forward(att(B=1, H=1, H_kv=1, **T), *[0] * 5) == NULL  # 2^24 - 2 blocks: fine
         assert g.gdn2_attention_forward(att(B=1, H=2, H_kv=1, **T), *[0] * 5) == UNSUPPORTED
+    # two threads for each of the forward's in the backward
+    assert g.gdn2_attention_backward(att(B=1, H=1, H_kv=1, T_q=2 ** 30 - 256, T_k=1), *[0] * 9, WS, 1 << 60) == NULL
+    assert g.gdn2_attention_backward(att(B=1, H=1, H_kv=1, T_q=1, T_k=2 ** 30 + 1), *[0] * 9, WS, 1 << 60) == UNSUPPORTED
     # packed: a block of room a sequence
     assert g.gdn2_attention_forward_varlen(att(B=2 ** 22, H=3, H_kv=1), *[0] * 7) == NULL
     assert g.gdn2_attention_forward_varlen(att(B=2 ** 22, H=4, H_kv=1), *[0] * 7) == UNSUPPORTED
@@ -158,7 +161,7 @@ def dec(N=4, H=8, H_kv=2, d=64, P=100, page=16, M=200, window=0, dtype=1, scale=
 BAD_DECODE = [(None, NULL), (dec(dtype=3), DTYPE), (dec(N=-1), SHAPE), (dec(P=-1), SHAPE), (dec(M=-1), SHAPE), (dec(H=0), SHAPE),
               (dec(H_kv=0), SHAPE), (dec(H=9), SHAPE), (dec(window=-1), SHAPE), (dec(page=0), SHAPE), (dec(scale=0.0), SHAPE),
               (dec(scale=NAN), SHAPE), (dec(d=32), UNSUPPORTED), (dec(page=48), UNSUPPORTED), (dec(M=2 ** 20, page=2048), UNSUPPORTED),
-              (dec(N=2 ** 22), UNSUPPORTED)]
+              (dec(N=2 ** 22), UNSUPPORTED), (dec(N=2 ** 19, M=1), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("desc,status", BAD_DECODE)
