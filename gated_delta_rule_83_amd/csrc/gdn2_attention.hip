@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
+    if (!find_block<kAttnRows>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
 }
 
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
-  const size_t tiles = attention_tiles(p.cu_q ? p.B : 1, p.Tq, p.cu_q != nullptr);
+  const size_t tiles = attention_blocks(p.cu_q ? p.B : 1, p.Tq, kAttnRows, p.cu_q != nullptr);
   const size_t units = (p.cu_q ? 1 : (size_t)p.B) * (size_t)p.H;
   if (!tiles || !units) return hipSuccess;
   attention_forward_kernel<BF16, D><<<(unsigned)(tiles * units), 256, 0, stream>>>(p, (unsigned)units);

@@ -9,7 +9,7 @@
 
 namespace gdn2 {
 
-constexpr int kAttnRows = 128;   // queries (forward, dq) or keys (dk, dv) of a workgroup
+constexpr int kAttnRows = 128;   // queries of a workgroup (forward, dq)
 
 struct AttentionArgs {
   int B, Tq, Tk, H, Hkv, d;   // packed: B sequences, Tq and Tk tokens in all
@@ -27,16 +27,20 @@ struct AttentionArgs {
   void *dq, *dk, *dv;
   float *delta;               // [lse] rowsum(dO o), from the dq pass to the dk, dv pass
   float *partial;             // parts > 1: [parts][2][rows of dk][Hkv * d]
-  int parts;                  // workgroups that share a key block's query heads
+  int keys, parts;            // AttentionSplit
 };
 
-// Query (or key) blocks of one head over the whole batch.
-inline size_t attention_tiles(int B, int T, bool packed) {
-  const size_t t = (size_t)T;
-  return packed ? t / kAttnRows + (size_t)B : (t + kAttnRows - 1) / kAttnRows * (size_t)B;
+// Blocks of `rows` queries (or keys) of one head: of one sequence, or (packed) of
+// all B, each with room for a ragged last one.
+inline size_t attention_blocks(int B, int T, int rows, bool packed) {
+  return packed ? (size_t)T / rows + (size_t)B : ((size_t)T + rows - 1) / rows;
 }
-// Workgroups that share a key block's query heads in the dk, dv pass.
-int attention_backward_parts(int B, int Tk, int H, int Hkv, bool packed);
+// The dk, dv pass: keys of a workgroup (64 or 128), and the workgroups that share
+// a key block's query heads.
+struct AttentionSplit {
+  int keys, parts;
+};
+AttentionSplit attention_backward_split(int B, int Tk, int H, int Hkv, int d, bool bf16, int window, bool packed);
 
 hipError_t launch_attention_forward(const AttentionArgs &p, hipStream_t stream);
 hipError_t launch_attention_backward(const AttentionArgs &p, hipStream_t stream);

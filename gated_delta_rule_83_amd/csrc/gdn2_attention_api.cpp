@@ -82,10 +82,10 @@ gdn2_status check_attention(const gdn2_attention_desc *d, bool packed, bool back
   const size_t es = size_of(d->dtype);
   if (d->stride_q * es % 16 || d->stride_k * es % 16 || d->stride_v * es % 16) return GDN2_ERR_BAD_SHAPE;
   if (d->T_q > INT32_MAX - 256 || d->T_k > INT32_MAX - 256) return GDN2_ERR_UNSUPPORTED;
-  // workgroups: blocks of 128 rows, and a head each; 512 threads in the backward
+  // workgroups: blocks of 128 rows, and a head each; in the backward, 512 threads or twice as many blocks of 64 keys
   const size_t most = backward ? kMaxGroups / 2 : kMaxGroups, B = (size_t)d->B;
   for (const int T : {d->T_q, d->T_k}) {
-    const size_t blocks = packed ? (size_t)T / gdn2::kAttnRows + B : ceil_div((size_t)T, gdn2::kAttnRows);
+    const size_t blocks = gdn2::attention_blocks(d->B, T, gdn2::kAttnRows, packed);
     if (blocks > most || B > most || blocks * (size_t)d->H > most || (!packed && blocks * (size_t)d->H * B > most))
       return GDN2_ERR_UNSUPPORTED;
   }
@@ -134,13 +134,14 @@ gdn2_status attention_forward(const gdn2_attention_desc *d, bool packed, const i
 // delta, lse in powers of two, and the parts' sums of dk and dv, each from a multiple of 16 bytes on
 struct BackwardSpace {
   size_t rows, partial, bytes;
-  int parts;
+  gdn2::AttentionSplit split;
 };
 BackwardSpace backward_space(const gdn2_attention_desc *d, bool packed) {
   BackwardSpace s;
   s.rows = ceil_div((size_t)q_rows(d, packed) * d->H * 4, 16) * 16;
-  s.parts = gdn2::attention_backward_parts(d->B, d->T_k, d->H, d->H_kv, packed);
-  s.partial = s.parts > 1 ? (size_t)s.parts * 2 * k_rows(d, packed) * d->H_kv * d->d * 4 : 0;
+  s.split = gdn2::attention_backward_split(d->B, d->T_k, d->H, d->H_kv, d->d, d->dtype == GDN2_BF16,
+                                           attention_args(d).window, packed);
+  s.partial = s.split.parts > 1 ? (size_t)s.split.parts * 2 * k_rows(d, packed) * d->H_kv * d->d * 4 : 0;
   s.bytes = 2 * s.rows + s.partial;
   return s;
 }
@@ -181,7 +182,8 @@ gdn2_status attention_backward(const gdn2_attention_desc *d, bool packed, const 
     p.delta = reinterpret_cast<float *>(at);
     p.lse = reinterpret_cast<float *>(at + s.rows);
     p.partial = reinterpret_cast<float *>(at + 2 * s.rows);
-    p.parts = s.parts;
+    p.keys = s.split.keys;
+    p.parts = s.split.parts;
   }
   return status_of(gdn2::launch_attention_backward(p, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
+    if (!find_block<kAttnRows>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
@@ -248,40 +248,41 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
 }
 
 // ---------------------------------------------------------------- dk, dv
-// 128 keys, 32 a pair of waves. The one keeps K and dv: scores, probabilities,
+// 128 or 64 keys, 32 a pair of waves. The one keeps K and dv: scores, probabilities,
 // dv += dO^T p; the other V and dk: dp, ds, dk += Q^T ds, one tile of queries
 // behind, with the probabilities from LDS (in fp32: a rounding of them would
 // stand beside the one of ds). So both have two products a tile and registers
 // for two waves a SIMD, one of each kind; with all four products and both
 // accumulators in one wave there is one a SIMD, whose vector instructions keep
 // the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us, so 665).
-template <bool BF16, int D>
-__global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionArgs p, unsigned units) {
+template <bool BF16, int D, int KEYS>
+__global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
+  constexpr int PAIRS = KEYS / 32, HALF = 64 * PAIRS;  // pairs of waves; threads of each kind
   constexpr int QT = 32, ES = BF16 ? 2 : 4, TILE = QT * L::ROW, RING = 3;
   constexpr int PROBS = 32 * 32 * 4;
   __shared__ __attribute__((aligned(16))) struct {
     char tile[RING][2][TILE];  // Q, dO
     float stat[RING][2][64];   // lse in powers of two and delta of a tile's rows (64 lanes land, 32 are used)
-    char probs[RING][4][PROBS];
-    uint32_t said[8];
+    char probs[RING][PAIRS][PROBS];
+    uint32_t said[2 * PAIRS];
   } sm;
   unsigned unit, rank;
   find_work(units, &unit, &rank);
   const int tile = (int)rank;  // causal: the first keys are seen most
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool second = wave >= 4;  // keeps V and dk
-  const int pair = wave & 3;
+  const bool second = wave >= PAIRS;  // keeps V and dk
+  const int pair = wave % PAIRS;
   const int group = p.H / p.Hkv, share = group / p.parts;  // query heads of a key head, and of this workgroup
   int seq, row0;
   const int slice = (int)(unit % (unsigned)p.parts);
   unsigned kvu = unit / (unsigned)p.parts;
   if (p.cu_q) {
-    if (!find_block(p.cu_k, p.B, p.Tk, tile, &seq, &row0)) return;
+    if (!find_block<KEYS>(p.cu_k, p.B, p.Tk, tile, &seq, &row0)) return;
   } else {
     seq = (int)(kvu / (unsigned)p.Hkv);
     kvu %= (unsigned)p.Hkv;
-    row0 = tile * kAttnRows;
+    row0 = tile * KEYS;
   }
   const int kv = (int)kvu, head0 = kv * group + slice * share;
   const Span sp = span_of(p, seq, head0);
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
   const Exponent<BF16> power(p.scale);
   const int first = m.first(row), last = m.last(row);
   // query tiles that some key of the workgroup is seen from; queries that see every one of them
-  const int blast = min(row0 + kAttnRows - 1, m.nk - 1);
+  const int blast = min(row0 + KEYS - 1, m.nk - 1);
   const int t_lo = m.first(row0) / QT, t_hi = (m.last(blast) + QT) / QT;
   const int b_lo = m.first(blast), b_hi = m.last(row0);
   auto hides = [&](int q0) { return q0 < b_lo || q0 + QT - 1 > b_hi; };
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
   const uint32_t at = lds_address(&sm), stats = lds_address(&sm.stat), probs = lds_address(&sm.probs) + pair * PROBS + lane * 16;
   const int nt = t_hi - t_lo, turns = nt > 0 ? nt * share : 0;
   // the first waves fetch Q, the second dO
-  Dma<BF16, D, QT> rows;
-  rows.init((second ? (int64_t)p.H * D : p.sq) * ES, tid & 255);
+  Dma<BF16, D, QT, HALF> rows;
+  rows.init((second ? (int64_t)p.H * D : p.sq) * ES, tid % HALF);
   const char *base = second ? static_cast<const char *>(p.dO) + (sp.q0 * (int64_t)p.H + head0) * D * ES
                             : static_cast<const char *>(p.q) + (sp.q0 * p.sq + (int64_t)head0 * D) * ES;
   // tile t of head head0 + hd into buffer `to`
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
     if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
   };
   auto scores = [&](int q0, int buf, auto masked) __attribute__((always_inline)) {
-    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 16 * h, pt = probs + buf * 4 * PROBS;
+    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 16 * h, pt = probs + buf * PAIRS * PROBS;
     floatx16 s = zero16();
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(512, 2) attention_dkv_kernel(const AttentionAr
     __builtin_amdgcn_s_setprio(0);
   };
   auto slopes = [&](int q0, int buf, auto masked) __attribute__((always_inline)) {
-    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 256 + 16 * h, pt = probs + buf * 4 * PROBS;
+    const uint32_t qt = at + 2 * buf * TILE, gt = qt + TILE, st = stats + buf * 512 + 256 + 16 * h, pt = probs + buf * PAIRS * PROBS;
     floatx16 s = zero16();
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -526,14 +527,18 @@ __global__ void __launch_bounds__(256) attention_outside_kernel(const AttentionA
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
   const bool packed = p.cu_q != nullptr;
   const size_t seqs = packed ? 1 : (size_t)p.B;
-  const size_t tq = attention_tiles(packed ? p.B : 1, p.Tq, packed), uq = seqs * (size_t)p.H;
+  const size_t tq = attention_blocks(packed ? p.B : 1, p.Tq, kAttnRows, packed), uq = seqs * (size_t)p.H;
   if (tq) {
     attention_dq_kernel<BF16, D><<<(unsigned)(tq * uq), 256, 0, stream>>>(p, (unsigned)uq);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  const size_t tk = attention_tiles(packed ? p.B : 1, p.Tk, packed), uk = seqs * (size_t)p.Hkv * (size_t)p.parts;
+  const size_t tk = attention_blocks(packed ? p.B : 1, p.Tk, p.keys, packed), uk = seqs * (size_t)p.Hkv * (size_t)p.parts;
   if (!tk) return hipSuccess;
-  attention_dkv_kernel<BF16, D><<<(unsigned)(tk * uk), 512, 0, stream>>>(p, (unsigned)uk);
+  // fp32 at d 128 has 128 keys alone: two workgroups of 64 do not fit a CU's LDS
+  if (p.keys == 64 && (BF16 || D == 64))
+    attention_dkv_kernel<BF16, D, BF16 || D == 64 ? 64 : 128><<<(unsigned)(tk * uk), 256, 0, stream>>>(p, (unsigned)uk);
+  else
+    attention_dkv_kernel<BF16, D, 128><<<(unsigned)(tk * uk), 512, 0, stream>>>(p, (unsigned)uk);
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (p.parts > 1) {
     const int64_t n = (int64_t)seqs * p.Tk * p.Hkv * D;
@@ -546,16 +551,25 @@ template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t s
 
 }  // namespace
 
-// A key block's workgroup walks the query heads that share it. Where there are
-// few such blocks the heads are dealt out to several workgroups, whose sums are
-// joined in order: 4 workgroups a CU even out blocks that are seen by many
-// queries and by few.
-int attention_backward_parts(int B, int Tk, int H, int Hkv, bool packed) {
-  const size_t blocks = (packed ? (size_t)Tk / kAttnRows + 1 : attention_tiles(1, Tk, false) * (size_t)B) * (size_t)Hkv;
+// Keys: 64 a workgroup, two of which share a CU and do not wait for each other, where d is 64 (B4 T4096 H32/4 bf16:
+// backward 1143 us, 1220 with 128), under a window (T4096 window 512 H16/2 d128: 707 against 793) and where 128 would
+// leave CUs without any; else 128, whose queries cross LDS once for twice as many keys (B4 T4096 H16/2 d128: 1025
+// against 1059).
+// Parts: a key block's workgroup walks the query heads that share it. Where there are few such blocks the heads are
+// dealt out to several workgroups, whose sums are joined in order: 1024 of 128 keys, or 2048 of 64, even out blocks
+// that are seen by many queries and by few (the d 64 shape above with 1024 of 64: 1217 us); under a window, where all
+// are seen alike, 512 are enough (the shape above with 2048 of 64: 744 us).
+AttentionSplit attention_backward_split(int B, int Tk, int H, int Hkv, int d, bool bf16, int window, bool packed) {
+  auto blocks = [&](int keys) {
+    return (packed ? (size_t)Tk / keys + 1 : attention_blocks(1, Tk, keys, false) * (size_t)B) * (size_t)Hkv;
+  };
   const int group = H / Hkv;
-  for (int parts = 1; parts < group; ++parts)
-    if (group % parts == 0 && blocks * parts >= 1024) return parts;
-  return group;
+  AttentionSplit s;
+  s.keys = (bf16 || d == 64) && (d == 64 || window || blocks(128) * group < 256) ? 64 : 128;
+  const size_t enough = window ? 512 : s.keys == 64 ? 2048 : 1024;
+  for (s.parts = 1; s.parts < group; ++s.parts)
+    if (group % s.parts == 0 && blocks(s.keys) * s.parts >= enough) break;
+  return s;
 }
 
 hipError_t launch_attention_backward(const AttentionArgs &p, hipStream_t stream) {

@@ -373,15 +373,16 @@ struct Mask {
 
 __device__ __forceinline__ int clamp_to(int x, int T) { return x < 0 ? 0 : (x > T ? T : x); }
 
-// Packed sequences: block slots s of sequence n are cu[n] / 128 + n .. , which
+// Packed sequences: block slots s of sequence n are cu[n] / ROWS + n .. , which
 // leaves every sequence room for its ragged last block; the workgroup finds n
 // by 64 tries at once.
+template <int ROWS>
 __device__ __forceinline__ bool find_block(const int32_t *cu, int B, int T, int s, int *seq, int *row0) {
   const int lane = threadIdx.x & 63;
   int lo = 0, cnt = B;
   while (cnt > 1) {
     const int step = (cnt + 63) >> 6, i = lane * step;
-    const bool below = i < cnt && clamp_to(cu[lo + min(i, cnt - 1)], T) / 128 + lo + i <= s;
+    const bool below = i < cnt && clamp_to(cu[lo + min(i, cnt - 1)], T) / ROWS + lo + i <= s;
     const uint64_t b = __ballot(below);
     const int c = b ? 63 - __builtin_clzll(b) : 0;
     lo = __builtin_amdgcn_readfirstlane(lo + c * step);
@@ -389,7 +390,7 @@ __device__ __forceinline__ bool find_block(const int32_t *cu, int B, int T, int 
     cnt = __builtin_amdgcn_readfirstlane(cnt);
   }
   *seq = lo;
-  *row0 = (s - (clamp_to(cu[lo], T) / 128 + lo)) * 128;
+  *row0 = (s - (clamp_to(cu[lo], T) / ROWS + lo)) * ROWS;
   return *row0 >= 0;
 }
 

@@ -66,6 +66,24 @@ def test_head_layouts(H, Hkv, dtype):
     check(f"attention heads {H}/{Hkv} {dtype}", q, k, v, dO, o, lse, gr)
 
 
+@pytest.mark.parametrize("d,H,Hkv,T,window,causal", [(128, 48, 4, 300, 0, True), (128, 64, 2, 260, 0, False),
+                                                      (64, 96, 16, 290, 50, True), (128, 120, 20, 640, 100, True)])
+def test_many_heads(d, H, Hkv, T, window, causal):
+    """Enough workgroups for key blocks of 128 rows, and for fewer parts than a key head has query heads."""
+    q, k, v, dO = problem(H + T, 1 if T > 300 else 2, T, T, H, Hkv, d, "bf16")
+    o, lse, gr = run(q, k, v, dO, window=window, causal=causal)
+    check(f"attention heads {H}/{Hkv} d{d} {window} {causal}", q, k, v, dO, o, lse, gr, causal, window)
+
+
+def test_many_heads_of_packed_sequences():
+    lengths = [140, 0, 128, 1, 200, 60]
+    q, k, v, dO, cu, _ = packed(12, lengths, lengths, 56, 4, 128, "bf16", front=2, behind=5)
+    o, lse = g.attention_forward_varlen(q, k, v, cu)
+    gr = g.attention_backward_varlen(q, k, v, o, lse, dO, cu)
+    torch.cuda.synchronize()
+    check_packed("packed, many heads", q, k, v, dO, cu, cu, o, lse, gr)
+
+
 LENGTHS = [[5], [0, 0, 3, 0], [128, 1, 127, 129, 0, 64], [300, 0, 1, 33, 250], [1] * 70, [0] * 5]
 
 
