@@ -216,7 +216,7 @@ gdn2_status check_store(const gdn2_kv_cache_desc *d, bool packed) {
   const int64_t w = (int64_t)d->H_kv * d->d;
   if (d->N < 0 || d->T < 0 || d->P < 0 || d->M < 0 || d->H_kv < 1 || d->page < 1 || (!packed && d->T != d->N)) return GDN2_ERR_BAD_SHAPE;
   if ((d->d != 64 && d->d != 128) || !power_of_two(d->page) || (int64_t)d->M * d->page > 1 << 30 || w > kMaxStride ||
-      d->stride_k > kMaxStride || d->stride_v > kMaxStride || d->T > INT32_MAX - 256)
+      d->stride_k > kMaxStride || d->stride_v > kMaxStride || d->T > INT32_MAX - 256 || d->N > INT32_MAX - 256)
     return GDN2_ERR_UNSUPPORTED;
   if ((d->stride_k && d->stride_k < w) || (d->stride_v && d->stride_v < w) || d->stride_k * size_of(d->dtype) % 16 ||
       d->stride_v * size_of(d->dtype) % 16)

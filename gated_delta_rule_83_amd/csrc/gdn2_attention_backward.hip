@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
 // stand beside the one of ds). So both have two products a tile and registers
 // for two waves a SIMD, one of each kind; with all four products and both
 // accumulators in one wave there is one a SIMD, whose vector instructions keep
-// the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us, so 665).
+// the matrix cores waiting (B4 T4096 H16/2 d128 bf16: 1061 us, so 640 to 674).
 template <bool BF16, int D, int KEYS>
 __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;

@@ -767,7 +767,7 @@ gdn2_status gdn2_attention_decode(const gdn2_attention_decode_desc *desc, const 
  * int32 device offsets into T packed tokens) or NULL (T = N, one token a
  * sequence); lengths[n] counts the sequence's tokens with the new ones, which are
  * its last. k, v : [T, H_kv, d]. Tokens of no sequence, before a sequence's
- * token 0, past the table, or of a page outside [0, P) are skipped; the rest of
+ * token 0, past the table, or of a page outside [0, P) are skipped; N, T up to 2^31 - 257; the rest of
  * the cache is left as it was. Precondition: no two tokens of a call have the
  * same place (sequences may share the pages that neither writes); where two do,
  * that place holds parts of either. */

@@ -198,7 +198,7 @@ def sto(N=3, T=50, H_kv=2, d=64, P=100, page=16, M=20, dtype=1, sk=0, sv=0):
     (None, NULL), (sto(dtype=2), DTYPE), (sto(N=-1), SHAPE), (sto(T=-1), SHAPE), (sto(P=-1), SHAPE), (sto(M=-1), SHAPE),
     (sto(H_kv=0), SHAPE), (sto(page=0), SHAPE), (sto(sk=64), SHAPE), (sto(sv=132), SHAPE), (sto(d=48), UNSUPPORTED),
     (sto(page=3), UNSUPPORTED), (sto(M=2 ** 21, page=1024), UNSUPPORTED), (sto(H_kv=2 ** 17), UNSUPPORTED),
-    (sto(T=2 ** 31 - 1), UNSUPPORTED)])
+    (sto(T=2 ** 31 - 1), UNSUPPORTED), (sto(N=2 ** 31 - 1), UNSUPPORTED)])
 def test_store_descriptions(desc, status):
     assert g.gdn2_kv_cache_store(desc, *fakes(7)) == status
 

@@ -143,6 +143,27 @@ def test_a_packed_sequence_is_the_sequence_alone():
         assert torch.equal(o[a:b], o1[0]) and torch.equal(lse[:, a:b], l1[0])
 
 
+@pytest.mark.parametrize("T,S", [(5, 0), (0, 5), (200, 0), (0, 200)])
+def test_no_keys_or_no_queries(T, S):
+    q, k, v, dO = problem(T + S, 2, T, S, 4, 2, 64, "bf16")
+    o, lse, gr = run(q, k, v, dO)
+    assert (o == 0).all() and (lse == -float("inf")).all()
+    assert all((x == 0).all() and x.shape == t.shape for x, t in zip(gr.values(), (q, k, v)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_query_that_is_no_number(dtype):
+    q, k, v, dO = problem(8, 1, 150, 150, 2, 1, 64, dtype)
+    q[0, 70, 1, 5] = float("nan")
+    o, lse, gr = run(q, k, v, dO)
+    assert torch.isnan(o[0, 70, 1]).all() and torch.isnan(lse[0, 1, 70])
+    o[0, 70, 1], lse[0, 1, 70] = 0, 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert torch.isnan(gr["dq"][0, 70, 1]).all() and torch.isfinite(gr["dq"][0, 70, 0]).all()
+    for nm in ("dk", "dv"):  # the keys that it sees
+        assert torch.isnan(gr[nm][0, :71]).all() and torch.isfinite(gr[nm][0, 71:]).all()
+
+
 def test_offsets_outside_the_tokens_are_clamped():
     q, k, v, dO, _, _ = packed(6, [200], [200], 2, 1, 64, "bf16")
     far = torch.tensor([-50, 120, 10 ** 9], dtype=torch.int32, device=DEV)

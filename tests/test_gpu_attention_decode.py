@@ -100,6 +100,20 @@ def test_bad_pages_and_lengths():
     check("decode bad pages", o[[0, 2]], q[[0, 2]], [tuple(x[keep] for x in toks[0]), toks[2]])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length", [1, 33, 100, 129, 3000])
+def test_scores_that_are_no_number(length, dtype):
+    """A query that is no number, and a last key that is alone in its wave: no result hides them."""
+    q, kc, vc, pages, ln, _ = problem(10, [length, length], 4, 2, 64, 32, dtype)
+    q[0, 0, 1, 7] = float("nan")
+    t = length - 1
+    kc[pages[1, t // 32].long(), 0, t % 32, 3] = float("nan")
+    o = g.attention_decode(q, kc, vc, pages, ln)
+    torch.cuda.synchronize()
+    assert torch.isnan(o[0, 0, 1]).all() and torch.isfinite(o[0, 0, [0, 2, 3]]).all()
+    assert torch.isnan(o[1, 0, :2]).all() and torch.isfinite(o[1, 0, 2:]).all()
+
+
 @pytest.mark.parametrize("page", [8, 64])
 def test_values_that_are_no_number(page):
     q, kc, vc, pages, ln, toks = problem(9, [100, 100], 4, 2, 64, page, "bf16")
