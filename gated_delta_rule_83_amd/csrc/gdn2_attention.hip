@@ -19,10 +19,13 @@ using namespace attn;
 // left out for nearly every tile.
 constexpr float kSlack = 8.f;
 
-template <bool BF16, int D>
+// SPLIT 2: 64 queries a workgroup; each 32 of them on two waves, which take half of
+// every tile's keys each and join their sums in the end.
+template <bool BF16, int D, int SPLIT>
 __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forward_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
-  constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4;  // 16 KB a tile of K or V at D = 128
+  constexpr int ROWS = kAttnRows / SPLIT, PAIRS = 4 / SPLIT;
+  constexpr int KT = BF16 || SPLIT == 2 ? 64 : 32, SUB = KT / 32 / SPLIT, ES = BF16 ? 2 : 4;
   constexpr int TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
     char tile[2][2][TILE];
@@ -34,12 +37,12 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block<kAttnRows>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
+    if (!find_block<ROWS>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
     head = (int)(unit % (unsigned)p.H);
-    row0 = tile * kAttnRows;
+    row0 = tile * ROWS;
   }
   const Span sp = span_of(p, seq, head);
   const Mask m = sp.m;
@@ -49,13 +52,14 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   const char *vbase = static_cast<const char *>(p.v) + (sp.k0 * p.sv + (int64_t)kv * D) * ES;
 
   // this lane's query, and the keys that it sees
-  const int mine = row0 + 32 * wave + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
+  const int part = SPLIT == 1 ? 0 : wave / PAIRS, half = part * 32 * SUB;  // of the tiles' keys, from the half'th on
+  const int mine = row0 + 32 * (wave % PAIRS) + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
   Frag<BF16> q[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
   arrived(q);
   const Exponent<BF16> power(p.scale);
   // tiles that some query of the workgroup sees; keys that every one of them sees
-  const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
+  const int blast = min(row0 + ROWS - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;  // hi = -1: none
   const int b_lo = m.lo(blast), b_hi = m.hi(row0);
   auto hides = [&](int key0) { return key0 < b_lo || key0 + KT - 1 > b_hi; };
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   Across<BF16, D> across;
   along.init(lane);
   across.init(lane);
-  const uint32_t at = lds_address(&sm);  // tile [i][j] from (2 i + j) TILE on
+  const uint32_t at = lds_address(&sm) + half * L::ROW;  // this wave's keys of tile [i][j] from (2 i + j) TILE on
   Dma<BF16, D, KT> ks, vs;
   ks.init(p.sk * ES, tid);
   vs.init(p.sv * ES, tid);
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
       const bool masked = hides(key0);
       if (careful && masked) clean<BF16, TILE>(sm.tile[BUF][1], tid);
       // (behind the last tile: scores of what the buffer holds, which nobody uses)
-      step(s[BUF], s[BUF ^ 1], at + (2 * BUF + 1) * TILE, at + 2 * (BUF ^ 1) * TILE, key0, masked);
+      step(s[BUF], s[BUF ^ 1], at + (2 * BUF + 1) * TILE, at + 2 * (BUF ^ 1) * TILE, key0 + half, masked);
     };
     for (int t = t_lo; t < t_hi; t += 2) {
       turn(t, std::integral_constant<int, 0>{});
@@ -199,8 +203,37 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
     if (!any_wave(any_odd(acc), sm.said, tid)) break;
   }
 
-  if (mine >= m.nq) return;
   sum = other_half_sum(sum);
+  if constexpr (SPLIT == 2) {
+    // the second half's maximum, sum and accumulator into the first's, through what was the tiles' memory
+    floatx4 *to = reinterpret_cast<floatx4 *>(&sm) + (wave % PAIRS) * (D / 32 * 4 + 1) * 64 + lane;
+    __syncthreads();
+    if (part) {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[(4 * b + i) * 64] = floatx4{acc[b][4 * i], acc[b][4 * i + 1], acc[b][4 * i + 2], acc[b][4 * i + 3]};
+      to[D / 32 * 4 * 64] = floatx4{top, sum, 0.f, 0.f};
+    }
+    __syncthreads();
+    if (part) return;
+    const floatx4 other = to[D / 32 * 4 * 64];
+    const float most = fmaxf(top, other[0]);
+    // a half that saw no number above -inf: its sums are zero or NaN
+    const float f = top == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(top - most);
+    const float g = other[0] == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(other[0] - most);
+    top = most;
+    sum = f * sum + g * other[1];
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const floatx4 x = to[(b * 4 + i / 4) * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][i + e] = f * acc[b][i + e] + g * x[e];
+      }
+  }
+  if (mine >= m.nq) return;
   const bool empty = hi < lo;  // no key at all: zero, and a log-sum of -inf
   char *out = static_cast<char *>(p.o) + ((sp.q0 + mine) * (int64_t)p.H + head) * D * ES;
   store_row<BF16, D>(out, acc, empty ? 0.f : 1.f / sum, h);
@@ -208,10 +241,20 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
 }
 
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
-  const size_t tiles = attention_blocks(p.cu_q ? p.B : 1, p.Tq, kAttnRows, p.cu_q != nullptr);
-  const size_t units = (p.cu_q ? 1 : (size_t)p.B) * (size_t)p.H;
-  if (!tiles || !units) return hipSuccess;
-  attention_forward_kernel<BF16, D><<<(unsigned)(tiles * units), 256, 0, stream>>>(p, (unsigned)units);
+  const bool packed = p.cu_q != nullptr;
+  auto tiles = [&](int rows) { return attention_blocks(packed ? p.B : 1, p.Tq, rows, packed); };
+  const size_t units = (packed ? 1 : (size_t)p.B) * (size_t)p.H;
+  if (!tiles(kAttnRows) || !units) return hipSuccess;
+  // Where blocks of 128 queries are no more than run at once, half as deep ones are done sooner (us, 128 queries / 64):
+  // B1 T4096 H16/2 d128 bf16 103 / 88, B1 T2048 H8/2 46 / 32, in fp32 297 / 170, B1 T200 H8 d64 9.8 / 7.1. Where there
+  // are more, keys cross LDS for twice as many queries (B2 T4096 H16/2 d128 156 / 174, B8 563 / 651). 512 run at once,
+  // 256 of fp32 at d 128 (B2 T2048 H16/2 332 / 362); if all are equally deep, 512 fill the card already (B1 T4096
+  // window 300 27.8 / 31.3).
+  const size_t enough = (!BF16 && D == 128) || p.window || !p.causal ? 256 : 512;
+  if (tiles(kAttnRows) * units <= enough)
+    attention_forward_kernel<BF16, D, 2><<<(unsigned)(tiles(kAttnRows / 2) * units), 256, 0, stream>>>(p, (unsigned)units);
+  else
+    attention_forward_kernel<BF16, D, 1><<<(unsigned)(tiles(kAttnRows) * units), 256, 0, stream>>>(p, (unsigned)units);
   return hipGetLastError();
 }
 

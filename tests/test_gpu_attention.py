@@ -75,6 +75,14 @@ def test_many_heads(d, H, Hkv, T, window, causal):
     check(f"attention heads {H}/{Hkv} d{d} {window} {causal}", q, k, v, dO, o, lse, gr, causal, window)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,window,causal", [(64, 0, True), (128, 0, True), (64, 90, True), (128, 0, False)])
+def test_more_blocks_than_run_at_once(d, window, causal, dtype):
+    q, k, v, dO = problem(d + window, 4, 131, 140, 72, 36, d, dtype)
+    o, lse, gr = run(q, k, v, dO, window=window, causal=causal)
+    check(f"attention blocks d{d} {window} {causal} {dtype}", q, k, v, dO, o, lse, gr, causal, window)
+
+
 def test_many_heads_of_packed_sequences():
     lengths = [140, 0, 128, 1, 200, 60]
     q, k, v, dO, cu, _ = packed(12, lengths, lengths, 56, 4, 128, "bf16", front=2, behind=5)
@@ -162,6 +170,23 @@ def test_a_query_that_is_no_number(dtype):
     assert torch.isnan(gr["dq"][0, 70, 1]).all() and torch.isfinite(gr["dq"][0, 70, 0]).all()
     for nm in ("dk", "dv"):  # the keys that it sees
         assert torch.isnan(gr[nm][0, :71]).all() and torch.isfinite(gr[nm][0, 71:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_hidden_values_in_more_blocks_than_run_at_once(dtype):
+    """Infinities and NaN that no query sees, and one that later queries see."""
+    q, k, v, _ = problem(9, 4, 200, 200, 72, 72, 64, dtype)
+    o, lse = g.attention_forward(q, k, v)
+    k[:, 150, :, 1], v[:, 151, :, 2], v[:, 199, :, 3] = float("nan"), float("inf"), -float("inf")
+    o2, lse2 = g.attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(o[:, :150], o2[:, :150]) and torch.equal(lse[:, :, :150], lse2[:, :, :150])
+    assert torch.isnan(o2[:, 150:]).all() and torch.isnan(lse2[:, :, 150:]).all()
+    k[:, 150, :, 1] = 0
+    o2, _ = g.attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    assert torch.isfinite(o2[:, :151]).all() and not torch.isfinite(o2[:, 151:, :, 2]).any()
+    assert torch.isfinite(o2[:, :199, :, 3]).all() and torch.isfinite(o2[:, :, :, 4:]).all()
 
 
 def test_offsets_outside_the_tokens_are_clamped():
