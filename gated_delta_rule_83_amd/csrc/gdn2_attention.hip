@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
   float top, sum;
   Along<BF16, D> along;
   Across<BF16, D> across;
-  along.init(lane);
-  across.init(lane);
-  const uint32_t at = lds_address(&sm) + half * L::ROW;  // this wave's keys of tile [i][j] from (2 i + j) TILE on
+  along.init(lane, half);
+  across.init(lane, half);
+  const uint32_t at = lds_address(&sm);  // tile [i][j] from (2 i + j) TILE on
   Dma<BF16, D, KT> ks, vs;
   ks.init(p.sk * ES, tid);
   vs.init(p.sv * ES, tid);

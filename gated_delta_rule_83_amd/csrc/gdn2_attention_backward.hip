@@ -54,13 +54,19 @@ template <bool BF16> struct Base {
 };
 
 // ---------------------------------------------------------------- dq
-template <bool BF16, int D>
+// SPLIT 2: 64 queries a workgroup, each 32 on two waves with half of a tile's keys
+// each, as in the forward where blocks are few (us: B1 T2048 H8/2 d128 bf16,
+// the whole backward, 129 / 107, fp32 1062 / 891; B2 T1003 H6/3 d64 fp32 window
+// 300 99 / 74).
+template <bool BF16, int D, int SPLIT>
 __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_kernel(const AttentionArgs p, unsigned units) {
   using L = Tile<BF16, D>;
-  constexpr int KT = BF16 ? 64 : 32, SUB = KT / 32, ES = BF16 ? 2 : 4, TILE = KT * L::ROW;
+  constexpr int ROWS = kAttnRows / SPLIT, PAIRS = 4 / SPLIT;
+  constexpr int KT = BF16 || SPLIT == 2 ? 64 : 32, SUB = KT / 32 / SPLIT, ES = BF16 ? 2 : 4, TILE = KT * L::ROW;
   __shared__ __attribute__((aligned(16))) struct {
     char tile[2][2][TILE];
     uint32_t said[4];
+    float delta[SPLIT == 2 ? 4 : 1][64];
   } sm;
   unsigned unit, rank;
   find_work(units, &unit, &rank);
@@ -68,12 +74,12 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block<kAttnRows>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
+    if (!find_block<ROWS>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
     head = (int)(unit % (unsigned)p.H);
-    row0 = tile * kAttnRows;
+    row0 = tile * ROWS;
   }
   const Span sp = span_of(p, seq, head);
   const Mask m = sp.m;
@@ -82,7 +88,8 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   const char *kbase = static_cast<const char *>(p.k) + (sp.k0 * p.sk + (int64_t)kv * D) * ES;
   const char *vbase = static_cast<const char *>(p.v) + (sp.k0 * p.sv + (int64_t)kv * D) * ES;
 
-  const int mine = row0 + 32 * wave + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
+  const int side = SPLIT == 1 ? 0 : wave / PAIRS, half = side * 32 * SUB;  // of the tiles' keys, from the half'th on
+  const int mine = row0 + 32 * (wave % PAIRS) + (lane & 31), row = min(mine, m.nq - 1), hi = m.hi(row), lo = m.lo(row);
   const int64_t place = ((sp.q0 + row) * (int64_t)p.H + head) * D * ES;  // the row in o, dO and dq
   Frag<BF16> q[D / 16], g[D / 16];
   load_row<BF16, D>(q, static_cast<const char *>(p.q) + ((sp.q0 + row) * p.sq + (int64_t)head * D) * ES, h);
@@ -101,7 +108,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   arrived(g);
   const Exponent<BF16> power(p.scale);
   const Base<BF16> lse(p.lse_in[sp.rows + row]);
-  const int blast = min(row0 + kAttnRows - 1, m.nq - 1);
+  const int blast = min(row0 + ROWS - 1, m.nq - 1);
   const int t_lo = m.lo(row0) / KT, t_hi = (m.hi(blast) + KT) / KT;
   const int b_lo = m.lo(blast), b_hi = m.hi(row0);
   auto hides = [&](int key0) { return key0 < b_lo || key0 + KT - 1 > b_hi; };
@@ -109,8 +116,8 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   floatx16 acc[D / 32];
   Along<BF16, D> along;
   Across<BF16, D> across;
-  along.init(lane);
-  across.init(lane);
+  along.init(lane, half);
+  across.init(lane, half);
   const uint32_t at = lds_address(&sm);  // tile [i][j] from (2 i + j) TILE on
   Dma<BF16, D, KT> ks, vs;
   ks.init(p.sk * ES, tid);
@@ -137,16 +144,18 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
           s = mma<BF16>(s, along.read(at, 32 * u, kk), q[kk]);
           dp = mma<BF16>(dp, along.read(at + TILE, 32 * u, kk), g[kk]);
         }
-        const int from = lo - t * KT - 4 * h, to = hi - t * KT - 4 * h;
+        const int from = lo - t * KT - half - 4 * h, to = hi - t * KT - half - 4 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           own += 32 * u + row_of(i, 0) < from || 32 * u + row_of(i, 0) > to ? 0.f : lse.probability(power, s[i]) * dp[i];
       }
     }
-    __syncthreads();
     delta = other_half_sum(own);
+    if constexpr (SPLIT == 2) sm.delta[wave][lane] = delta;
+    __syncthreads();
+    if constexpr (SPLIT == 2) delta += sm.delta[(wave + PAIRS) % 4][lane];
   }
-  if (mine < m.nq && h == 0) {
+  if (mine < m.nq && h == 0 && side == 0) {
     p.delta[sp.rows + mine] = delta;
     p.lse[sp.rows + mine] = BF16 ? lse.high : p.lse_in[sp.rows + mine];
   }
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
       Frag<BF16> ds[SUB][2], rest[SUB][2];
       if (hides(key0)) {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) part(ds[u], rest[u], kt, vt, u, key0, std::true_type{});
+        for (int u = 0; u < SUB; ++u) part(ds[u], rest[u], kt, vt, u, key0 + half, std::true_type{});
         if (careful) {  // the scores take K as it is, the product without its odd values
           __syncthreads();
           clean<BF16, TILE>(sm.tile[BUF][0], tid);
@@ -218,10 +227,10 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
         for (int u = 0; u < SUB; ++u) product(ds[u], rest[u], kt, u, std::true_type{});
       } else {
         // each 32 keys' product beside the next ones' scores
-        part(ds[0], rest[0], kt, vt, 0, key0, std::false_type{});
+        part(ds[0], rest[0], kt, vt, 0, key0 + half, std::false_type{});
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-          if (u + 1 < SUB) part(ds[u + 1], rest[u + 1], kt, vt, u + 1, key0, std::false_type{});
+          if (u + 1 < SUB) part(ds[u + 1], rest[u + 1], kt, vt, u + 1, key0 + half, std::false_type{});
           product(ds[u], rest[u], kt, u, std::false_type{});
         }
       }
@@ -243,6 +252,21 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
       break;
     }
     if (!any_wave(any_odd(acc), sm.said, tid)) break;
+  }
+  if constexpr (SPLIT == 2) {  // the second half's sums into the first's, through what was the tiles' memory
+    floatx4 *to = reinterpret_cast<floatx4 *>(&sm) + (wave % PAIRS) * (D / 32 * 4) * 64 + lane;
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (side) to[(4 * b + i) * 64] = floatx4{acc[b][4 * i], acc[b][4 * i + 1], acc[b][4 * i + 2], acc[b][4 * i + 3]};
+    __syncthreads();
+    if (side) return;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[b][i] += to[(4 * b + i / 4) * 64][i % 4];
   }
   if (mine < m.nq) store_row<BF16, D>(static_cast<char *>(p.dq) + place, acc, p.scale, h);
 }
@@ -527,9 +551,15 @@ __global__ void __launch_bounds__(256) attention_outside_kernel(const AttentionA
 template <bool BF16, int D> hipError_t run(const AttentionArgs &p, hipStream_t stream) {
   const bool packed = p.cu_q != nullptr;
   const size_t seqs = packed ? 1 : (size_t)p.B;
-  const size_t tq = attention_blocks(packed ? p.B : 1, p.Tq, kAttnRows, packed), uq = seqs * (size_t)p.H;
-  if (tq) {
-    attention_dq_kernel<BF16, D><<<(unsigned)(tq * uq), 256, 0, stream>>>(p, (unsigned)uq);
+  auto tiles = [&](int rows) { return attention_blocks(packed ? p.B : 1, p.Tq, rows, packed); };
+  const size_t uq = seqs * (size_t)p.H;
+  if (tiles(kAttnRows)) {
+    // as in the forward
+    const size_t enough = (!BF16 && D == 128) || p.window || !p.causal ? 256 : 512;
+    if (tiles(kAttnRows) * uq <= enough)
+      attention_dq_kernel<BF16, D, 2><<<(unsigned)(tiles(kAttnRows / 2) * uq), 256, 0, stream>>>(p, (unsigned)uq);
+    else
+      attention_dq_kernel<BF16, D, 1><<<(unsigned)(tiles(kAttnRows) * uq), 256, 0, stream>>>(p, (unsigned)uq);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   const size_t tk = attention_blocks(packed ? p.B : 1, p.Tk, p.keys, packed), uk = seqs * (size_t)p.Hkv * (size_t)p.parts;

@@ -117,19 +117,20 @@ template <class V> __device__ __forceinline__ V lds_read(uint32_t at) {
 }
 
 // A lane's places in a tile. Rows 16 apart are exchanged alike, so the places of
-// rows r .. r + 15 serve all the others: what a read adds is a constant.
+// rows r .. r + 15 serve all the others: what a read adds is a constant. `first`
+// (a multiple of 32, below the tile's rows): the row that counts as row 0.
 // LEAN (fp32): addresses are computed at every read; kept over a loop, as the compiler would, they take 2 registers a
 // step and 8 a block.
 template <bool BF16, int D, bool LEAN = false> struct Along {  // rows as rows or columns of an operand, contracted along them
   using L = Tile<BF16, D>;
   uint32_t off[BF16 ? D / 16 : 1];
-  __device__ __forceinline__ void init(int lane) {
+  __device__ __forceinline__ void init(int lane, int first = 0) {
     const int r = lane & 31, h = lane >> 5;
     if constexpr (BF16) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) off[kk] = L::at(r, 2 * kk + h);
+      for (int kk = 0; kk < D / 16; ++kk) off[kk] = L::at(r, 2 * kk + h) + first * L::ROW;
     } else {
-      off[0] = L::at(r, 2 * h);  // step kk: chunk 4 kk on top, in bits of its own
+      off[0] = L::at(r, 2 * h) + first * L::ROW;  // step kk: chunk 4 kk on top, in bits of its own
     }
   }
   // row r0 + (lane & 31), values 16 kk + 8 h ..; tile: LDS address; r0 a multiple of 16
@@ -153,17 +154,17 @@ template <bool BF16, int D, bool LEAN = false> struct Along {  // rows as rows o
 template <bool BF16, int D, bool LEAN = false> struct Across {
   using L = Tile<BF16, D>;
   uint32_t off[D / 32][BF16 ? 2 : 1];
-  __device__ __forceinline__ void init(int lane) {
+  __device__ __forceinline__ void init(int lane, int first = 0) {
     const int h = lane >> 5;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b) {
       if constexpr (BF16) {
         const int col = 32 * b + 16 * ((lane >> 4) & 1) + 4 * (lane & 3), r = 4 * h + ((lane >> 2) & 3);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) off[b][e] = L::at(r + 8 * e, col >> 3) + 2 * (col & 7);
+        for (int e = 0; e < 2; ++e) off[b][e] = L::at(r + 8 * e, col >> 3) + 2 * (col & 7) + first * L::ROW;
       } else {
         const int col = 32 * b + (lane & 31);
-        off[b][0] = L::at(4 * h, col >> 2) + 4 * (col & 3);
+        off[b][0] = L::at(4 * h, col >> 2) + 4 * (col & 3) + first * L::ROW;
       }
     }
   }
