@@ -70,11 +70,11 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   } sm;
   unsigned unit, rank;
   find_work(units, &unit, &rank);
-  const int tile = (int)(gridDim.x / units - 1 - rank);  // causal: the last block sees most
+  const int slots = (int)(gridDim.x / units), tile = slots - 1 - (int)rank;  // causal: the last block sees most
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int seq, row0, head;
   if (p.cu_q) {
-    if (!find_block<ROWS>(p.cu_q, p.B, p.Tq, tile, &seq, &row0)) return;
+    if (!find_ranked<ROWS, false>(p, slots, (int)rank, &seq, &row0)) return;
     head = (int)unit;
   } else {
     seq = (int)(unit / (unsigned)p.H);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const Attent
   const int slice = (int)(unit % (unsigned)p.parts);
   unsigned kvu = unit / (unsigned)p.parts;
   if (p.cu_q) {
-    if (!find_block<KEYS>(p.cu_k, p.B, p.Tk, tile, &seq, &row0)) return;
+    if (!find_ranked<KEYS, true>(p, 0, tile, &seq, &row0)) return;
   } else {
     seq = (int)(kvu / (unsigned)p.Hkv);
     kvu %= (unsigned)p.Hkv;

@@ -404,6 +404,53 @@ __device__ __forceinline__ void find_work(unsigned units, unsigned *unit, unsign
   *unit = units % 8 ? i : (i & 7) * (units >> 3) + (i >> 3);
 }
 
+// The rank'th block of packed sequences, from the one with the most to do on: find_block takes the last sequence
+// first, and a long one near the front is begun when the rest is nearly done. For causal attention of up to 64
+// sequences the blocks are counted by level instead (KEYS: of keys, whose first block is seen by most queries; else of
+// queries, whose last block sees most keys, the prefix included): lane n holds sequence n's blocks nb and its lowest
+// level c, and the level that the rank falls into is found by halves (us, before and so: 8 sequences, the longest 6266 of
+// 32768 tokens, H8/2 d64: forward 247 / 209, backward 827 / 708; 24 of 16384 H16/4 d128: 145 / 143, 542 / 499; 64 of
+// 32768 H16/2: 216 / 220, 806 / 726).
+template <int ROWS, bool KEYS>
+__device__ __forceinline__ bool find_ranked(const AttentionArgs &p, int slots, int rank, int *seq, int *row0) {
+  const int32_t *cu = KEYS ? p.cu_k : p.cu_q;
+  const int T = KEYS ? p.Tk : p.Tq;
+  if (!p.causal || p.window || p.B > 64) return find_block<ROWS>(cu, p.B, T, KEYS ? rank : slots - 1 - rank, seq, row0);
+  const int lane = threadIdx.x & 63;
+  int nb = 0, c = 0;
+  if (lane < p.B) {
+    const int n = max(clamp_to(cu[lane + 1], T) - clamp_to(cu[lane], T), 0);
+    nb = n / ROWS + (n % ROWS != 0);
+    if (!KEYS && p.cu_k != p.cu_q) {
+      const int nk = max(clamp_to(p.cu_k[lane + 1], p.Tk) - clamp_to(p.cu_k[lane], p.Tk), 0);
+      c = max(nk - n, 0) / ROWS;
+    }
+  }
+  // blocks of level x and above: a wave's sum
+  auto count = [&](int x) {
+    int sum = min(max(nb + c - x, 0), nb);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xf, 0xf, true);  // lanes of a row of 16, 1, 2, 4, 8 apart
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xf, 0xf, true);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xf, 0xf, true);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xf, 0xf, true);
+    return __builtin_amdgcn_readlane(sum, 15) + __builtin_amdgcn_readlane(sum, 31) + __builtin_amdgcn_readlane(sum, 47) +
+           __builtin_amdgcn_readlane(sum, 63);
+  };
+  if (count(0) <= rank) return false;  // no more blocks
+  // the highest level that has the rank'th block at or above it
+  int at = 0;
+  for (int step = 1 << (31 - __builtin_clz((unsigned)(((int64_t)p.Tq + p.Tk) / ROWS) + 1u)); step; step >>= 1)
+    if (count(at + step) > rank) at += step;
+  const int left = rank - count(at + 1);
+  const bool on = at >= c && at < c + nb;
+  const uint64_t all = __ballot(on);
+  const int n = __builtin_ctzll(__ballot(on && __builtin_popcountll(all & ((1ull << lane) - 1)) == left));
+  const int block = at - __builtin_amdgcn_readlane(c, n);
+  *seq = n;
+  *row0 = (KEYS ? __builtin_amdgcn_readlane(nb, n) - 1 - block : block) * ROWS;
+  return true;
+}
+
 // A sequence's tokens: the first query and key over the whole batch, how many there are, and
 // the first of `head`'s values of a [head, query] array (lse, delta).
 struct Span {
