@@ -19,6 +19,12 @@
 // of 4096 causal tokens are 1.25 times as far off as their own rounding, of 200
 // tokens 1.06 times, where one operand leaves 1.45 and 1.47; it costs 2% (B4
 // T4096 H16/2 d128: 984 -> 1005 us).
+//
+// A query that sees one key has p = 1 and delta = dp: ds is zero (or NaN), of
+// which two orders of the sums would leave noise, with nothing beside it where
+// every query sees one. So dq's row, or all of dk, is multiplied by zero in the
+// end; where one query does, the first key's own, its ds is in dk (in a partly
+// hidden tile, the only kind that can hold it).
 #include "gdn2_attention_device.hpp"
 
 namespace gdn2 {
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][i] += to[(4 * b + i / 4) * 64][i % 4];
   }
-  if (mine < m.nq) store_row<BF16, D>(static_cast<char *>(p.dq) + place, acc, p.scale, h);
+  if (mine < m.nq) store_row<BF16, D>(static_cast<char *>(p.dq) + place, acc, lo == hi ? 0.f : p.scale, h);
 }
 
 // ---------------------------------------------------------------- dk, dv
@@ -324,6 +330,8 @@ __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const Attent
   const int t_lo = m.first(row0) / QT, t_hi = (m.last(blast) + QT) / QT;
   const int b_lo = m.first(blast), b_hi = m.last(row0);
   auto hides = [&](int q0) { return q0 < b_lo || q0 + QT - 1 > b_hi; };
+  const bool all_lone = m.nk == 1 || m.window == 1;  // every query sees one key
+  const int lone = m.causal ? -m.shift : -1;         // else the query that does
 
   floatx16 acc[D / 32];
   constexpr bool LEAN = !BF16 && D == 128;
@@ -415,7 +423,10 @@ __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const Attent
     for (int i = 0; i < 16; i += 4) {
       const floatx4 d = lds_read<floatx4>(st + 4 * row_of(i, 0)), w = lds_read<floatx4>(pt + i * 256);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i + e] = w[e] * (s[i + e] - d[e]);
+      for (int e = 0; e < 4; ++e) {
+        const bool alone = decltype(masked)::value && row_of(i, 0) + e == lone - q0 - 4 * h;
+        s[i + e] = (alone ? 0.f : w[e]) * (s[i + e] - d[e]);
+      }
     }
     if constexpr (decltype(masked)::value) {
 #pragma unroll
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const Attent
     if (!any_wave(any_odd(acc), sm.said, tid)) break;
   }
   if (mine >= m.nk) return;
-  const float f = second ? p.scale : 1.f;
+  const float f = !second ? 1.f : all_lone ? 0.f : p.scale;
   const int64_t to = ((sp.k0 + mine) * (int64_t)p.Hkv + kv) * D;
   if (p.parts == 1) {
     store_row<BF16, D>(static_cast<char *>(second ? p.dk : p.dv) + to * ES, acc, f, h);

@@ -725,8 +725,9 @@ gdn2_status gdn2_attention_forward_varlen(const gdn2_attention_desc *desc, const
 /* Gradients of the forward calls, from their inputs, o and lse, given dO (like
  * o): dq like o, dk and dv [B, T_k, H_kv, d] (the sums over the query heads that
  * share a key head). workspace: ..._workspace_bytes(desc) bytes, 16-byte aligned.
- * Packed gradient rows outside every sequence are zero. Results are
- * deterministic (no atomics). */
+ * Packed gradient rows outside every sequence are zero. A query that sees one
+ * key alone leaves exactly nothing in dq and dk (its probability is 1 whatever
+ * they are). Results are deterministic (no atomics). */
 size_t gdn2_attention_backward_workspace_bytes(const gdn2_attention_desc *desc);
 gdn2_status gdn2_attention_backward(const gdn2_attention_desc *desc, const void *q, const void *k, const void *v,
                                     const void *o, const float *lse, const void *dO, void *dq, void *dk, void *dv,
