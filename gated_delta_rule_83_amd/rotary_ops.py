@@ -91,7 +91,7 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_
                                  _ptr(q_out), _ptr(k_out) if k is not None else None, handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
-    return desc, q_out, k_out if k is not None else None
+    return q_out, k_out if k is not None else None
 
 
 def rotary_forward(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
@@ -100,7 +100,7 @@ def rotary_forward(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps:
     tokens lie apart, as of a fused projection, are taken as they are),
     positions [...] int32, inv_freq [rot / 2] fp32, weights [d] of one type or
     None. Returns (q_out, k_out), contiguous."""
-    return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_out, k_out, stream)[1:]
+    return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_out, k_out, stream)
 
 
 def rotary_backward(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, eps: float = 1e-6, norm: bool = True,
@@ -155,7 +155,8 @@ def _autograd_function():
 
         @staticmethod
         def forward(ctx, q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs):
-            ctx.desc, qo, ko = _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, None, None, None)
+            qo, ko = _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, None, None, None)
+            ctx.problem = eps, norm, pairs
             ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
             return qo, ko
 
@@ -164,11 +165,13 @@ def _autograd_function():
             # autograd has made the forward's device and stream current
             no_second_order("rotary")
             q, k, positions, inv_freq, qw, kw = ctx.saved_tensors
+            # hooks on saved tensors may return them laid out otherwise than the forward's
+            desc, _ = _problem(q, k, positions, inv_freq, qw, kw, *ctx.problem)
             new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
             dq, dk = new(q), None if k is None else new(k)
             dqw = new(qw) if ctx.needs_input_grad[4] else None
             dkw = new(kw) if ctx.needs_input_grad[5] else None
-            _launch_backward(ctx.desc, q, k, qw, kw, positions, inv_freq, gq.contiguous(),
+            _launch_backward(desc, q, k, qw, kw, positions, inv_freq, gq.contiguous(),
                              None if k is None else gk.contiguous(), (dq, dk, dqw, dkw), None,
                              torch._C._cuda_getCurrentRawStream(q.device.index))
             return dq, dk, None, None, dqw, dkw, None, None, None

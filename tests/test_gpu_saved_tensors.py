@@ -42,3 +42,26 @@ def test_attention(packed, kind, dtype):
     got = finish()
     torch.cuda.synchronize()
     assert torch.equal(got, plain)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["clone", "cpu"])
+def test_rotary(kind, dtype):
+    torch.manual_seed(2)
+    x, w = torch.randn(2, 150, (H + 2 * HK) * D, device=DEV).to(TYPES[dtype]), torch.randn(D, device=DEV)
+    pos = torch.arange(300, dtype=torch.int32, device=DEV).view(2, 150)
+    f = 1e4 ** (-torch.arange(0, D, 2, device=DEV) / D)
+    gq, gk = (torch.randn(2, 150, h, D, device=DEV).to(x.dtype) for h in (H, HK))
+
+    def step():
+        leaf, weight = x.clone().requires_grad_(), w.clone().requires_grad_()
+        q, k, _ = parts(leaf)
+        out = g.rotary(q, k, pos, f, weight, weight)
+        return lambda: torch.autograd.grad(out, (leaf, weight), (gq, gk))
+
+    plain = step()()
+    with hooks(kind):
+        finish = step()
+    got = finish()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, plain))

@@ -66,3 +66,22 @@ def test_attention(recorded, packed, hooked):
     for p, stride, heads in zip(ptrs[2 * packed:], (bwd.stride_q, bwd.stride_k, bwd.stride_v), (H, HK, HK)):
         assert seen[p].shape[-2] == heads and stride == seen[p].stride(-3)
     assert leaf.grad.shape == leaf.shape
+
+
+@pytest.mark.parametrize("hooked", [False, True])
+def test_rotary(recorded, hooked):
+    leaf, (q, k, _) = parts((2, 5))
+    seen = {}
+
+    def unpack(t):
+        t = t.clone() if hooked else t
+        seen[t.data_ptr()] = t
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+        a, b = g.rotary(q, k, torch.zeros(2, 5, dtype=torch.int32), torch.ones(D // 2))
+    (a.sum() + b.sum()).backward()
+    (_, fwd, _), (name, bwd, ptrs) = recorded
+    assert "backward" in name and (fwd.stride_q, fwd.stride_k) == ((H + 2 * HK) * D,) * 2
+    for p, stride, heads in zip(ptrs, (bwd.stride_q, bwd.stride_k), (H, HK)):
+        assert seen[p].shape[-2] == heads and stride == seen[p].stride(-3)
