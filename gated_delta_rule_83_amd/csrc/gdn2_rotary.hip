@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(256, P::WIDE ? 5 : 2) rotary_backward_kernel(c
       }
       float r = 1.f;
       if (p.norm) r = 1.f / __builtin_sqrtf(x.dot(x) / (float)p.d + p.eps);
+      r = live ? r : 0.f;  // lanes without a head: 1 / 0 where eps is, and NaN times zero in a weight's sum
 #pragma unroll
       for (int j = 0; j < P::PAIRS; ++j) {
         const float a = g.a[j] * turn.c[j] + g.b[j] * turn.s[j], b = g.b[j] * turn.c[j] - g.a[j] * turn.s[j];

@@ -197,3 +197,18 @@ def test_a_bad_row_stays_alone_and_graphs_repeat():
     keep = torch.ones(300, 4, dtype=torch.bool, device=DEV)
     keep[7, 2] = False
     assert torch.equal(a[keep], a3[keep]) and torch.equal(b, b3) and torch.isnan(a3[7, 2]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,H,Hk,d", [(5, 4, 1, 64), (40, 16, 2, 128), (3000, 3, 2, 64), (7, 1, 1, 32), (9, 2, 1, 256), (4, 2, 1, 62)])
+def test_no_epsilon(N, H, Hk, d, dtype):
+    """eps = 0, and heads that leave lanes of a wave without one: a weight's gradient takes nothing from those."""
+    rng = np.random.default_rng(N + d)
+    q, k, gq, gk = (rand(rng, N, h, d, dtype=dtype) for h in (H, Hk, H, Hk))
+    qw, kw, f = 1 + 0.2 * rand(rng, d, dtype="f32"), rand(rng, d, dtype="f32"), freqs(d)
+    pos = torch.arange(N, dtype=torch.int32, device=DEV)
+    qo, ko = g.rotary_forward(q, k, pos, f, qw, kw, eps=0.0)
+    gr = g.rotary_backward(q, k, pos, f, qw, kw, gq, gk, eps=0.0)
+    torch.cuda.synchronize()
+    one("rotary eps 0 q", q, qw, pos, f, 0.0, True, "halves", qo, gq, gr["dq"], gr["dq_weight"])
+    one("rotary eps 0 k", k, kw, pos, f, 0.0, True, "halves", ko, gk, gr["dk"], gr["dk_weight"])
