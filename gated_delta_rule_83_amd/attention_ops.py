@@ -4,7 +4,8 @@ token over a paged key-value cache, and that cache's writes.
 
 Query i of T_q stands at place i + T_k - T_q of its keys; causal queries see the
 keys up to their place, with window > 0 the last `window` of those. A query that
-sees nothing gives o = 0 and lse = -inf. `scale` defaults to 1 / sqrt(d).
+sees nothing (or scores of -inf alone) gives o = 0 and lse = -inf. `scale`
+defaults to 1 / sqrt(d).
 
 q, k and v may be views whose tokens lie apart (parts of a fused projection), as
 long as a token's heads are contiguous; results are contiguous.

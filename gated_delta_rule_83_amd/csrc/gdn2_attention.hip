@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
       }
   }
   if (mine >= m.nq) return;
-  const bool empty = hi < lo;  // no key at all: zero, and a log-sum of -inf
+  // no key at all, or scores of -inf alone: zero, and a log-sum of -inf
+  const bool empty = sum == 0.f;
   char *out = static_cast<char *>(p.o) + ((sp.q0 + mine) * (int64_t)p.H + head) * D * ES;
   store_row<BF16, D>(out, acc, empty ? 0.f : 1.f / sum, h);
   if (h == 0 && p.lse) p.lse[sp.rows + mine] = empty ? neg_inf() : __builtin_fmaf(top, kLn2, __builtin_fmaf(top, kLn2Low, __logf(sum)));

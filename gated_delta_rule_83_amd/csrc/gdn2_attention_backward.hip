@@ -33,15 +33,17 @@ namespace {
 using namespace attn;
 
 // A row's lse in powers of two; in fp32 in two parts, as the factor of its scores.
+// A row without any weight (lse -inf) has probabilities of zero, as +inf makes them.
+__device__ __forceinline__ float base_of(float lse) { return lse == neg_inf() ? -lse : lse; }
+
 template <bool BF16> struct Base {
   float high, low;
   Base() = default;
   __device__ __forceinline__ explicit Base(float lse) {
-    high = lse * kLog2e;
-    low = BF16 || lse == neg_inf() ? 0.f : __builtin_fmaf(lse, kLog2eLow, __builtin_fmaf(lse, kLog2e, -high));
+    *this = at(BF16 ? base_of(lse) * kLog2e : base_of(lse));
     pin_regs(high);
   }
-  // from what the first pass leaves: powers of two in bf16, lse itself in fp32
+  // from what the first pass leaves: powers of two in bf16, base_of(lse) in fp32
   static __device__ __forceinline__ Base at(float left) {
     Base b;
     if constexpr (BF16) {
@@ -49,7 +51,7 @@ template <bool BF16> struct Base {
       b.low = 0.f;
     } else {
       b.high = left * kLog2e;
-      b.low = left == neg_inf() ? 0.f : __builtin_fmaf(left, kLog2eLow, __builtin_fmaf(left, kLog2e, -b.high));
+      b.low = left == -neg_inf() ? 0.f : __builtin_fmaf(left, kLog2eLow, __builtin_fmaf(left, kLog2e, -b.high));
     }
     return b;
   }
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
   }
   if (mine < m.nq && h == 0 && side == 0) {
     p.delta[sp.rows + mine] = delta;
-    p.lse[sp.rows + mine] = BF16 ? lse.high : p.lse_in[sp.rows + mine];
+    p.lse[sp.rows + mine] = BF16 ? lse.high : base_of(p.lse_in[sp.rows + mine]);
   }
 
   // ds of 32 keys

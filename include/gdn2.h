@@ -690,7 +690,9 @@ gdn2_status gdn2_rotary_backward(const gdn2_rotary_desc *desc, const void *q, co
  * Query i of T_q stands at place i + T_k - T_q of the key axis (queries are the
  * last tokens of their keys, so keys may hold a prefix). It sees all keys, or
  * (causal) those up to its place, or (window > 0, causal only) the last `window`
- * of those. A query that sees no key gives o = 0 and lse = -inf, and no gradient.
+ * of those. A query that sees no key, or only scores of -inf (infinite or
+ * overflowing products), gives o = 0 and lse = -inf, and its probabilities are
+ * zero in the gradients.
  *   q : [B, T_q, H, d]   k, v : [B, T_k, H_kv, d]   o : [B, T_q, H, d]   in dtype
  *   lse : [B, H, T_q] fp32, may be NULL in the forward
  * d 64 or 128 (GDN2_ERR_UNSUPPORTED otherwise); scale > 0, finite; any B, T >= 0 with
