@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
         vs.load(sm.tile[0][1], vbase, t * KT, m.nk, wave);
         landed();
         __syncthreads();
-        poison<BF16, D, KT>(acc, sm.tile[0][1], lo - t * KT, hi - t * KT, h);
+        restore<BF16, D, KT, true>(acc, sm.tile[0][1], max(lo - t * KT, half), min(hi - t * KT, half + 32 * SUB - 1), h);
       }
       break;
     }

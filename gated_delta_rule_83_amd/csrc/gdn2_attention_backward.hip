@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
     __syncthreads();
     if constexpr (SPLIT == 2) delta += sm.delta[(wave + PAIRS) % 4][lane];
   }
+  delta += 0.f * delta;  // of an infinite dO: NaN, whatever of dp - delta the dk, dv pass would make of it
   if (mine < m.nq && h == 0 && side == 0) {
     p.delta[sp.rows + mine] = delta;
     p.lse[sp.rows + mine] = BF16 ? lse.high : base_of(p.lse_in[sp.rows + mine]);
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_dq_ker
         ks.load(sm.tile[0][0], kbase, t * KT, m.nk, wave);
         landed();
         __syncthreads();
-        poison<BF16, D, KT>(acc, sm.tile[0][0], lo - t * KT, hi - t * KT, h);
+        restore<BF16, D, KT, false>(acc, sm.tile[0][0], lo - t * KT, hi - t * KT, h);
       }
       break;
     }
@@ -510,7 +511,8 @@ __global__ void __launch_bounds__(4 * KEYS, 2) attention_dkv_kernel(const Attent
         fetch(i / nt, t_lo + i % nt, 0);
         landed();
         __syncthreads();
-        poison<BF16, D, QT>(acc, sm.tile[0][second ? 0 : 1], first - q0, last - q0, h);
+        if (second) restore<BF16, D, QT, false>(acc, sm.tile[0][0], first - q0, last - q0, h);
+        else restore<BF16, D, QT, true>(acc, sm.tile[0][1], first - q0, last - q0, h);
       }
       break;
     }

@@ -284,10 +284,12 @@ template <bool BF16, int D> __device__ __forceinline__ void store_row(char *row,
 // ---------------------------------------------------------------- values in hidden places
 // In a tile of which some places are hidden, an infinity or NaN there must leave
 // nothing, though 0 times it is NaN, and one in a place that a row sees must
-// make that row's result NaN in its column. A workgroup computes as if there
+// reach that row's result in its column. A workgroup computes as if there
 // were none; if a result is no number in the end (rare), it computes once more
 // with such tiles' odd values replaced by zero (clean), then looks through those
-// tiles again and puts NaN into the results that see one (poison).
+// tiles again for the odd values that a result sees (restore): weighted by a
+// probability, which is above zero, they are added as they are; weighted by a
+// gradient of a score, NaN stands for them, as their scores are not finite.
 __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {  // sign bits of the bf16 halves that are no number
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
@@ -328,9 +330,9 @@ template <int N> __device__ __forceinline__ bool any_odd(const floatx16 (&acc)[N
   return f;
 }
 
-// Rows first .. last of the tile are those this lane's column sees.
-template <bool BF16, int D, int R>
-__device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const char *t, int first, int last, int h) {
+// Rows first .. last of the tile are those this lane's column sees. ADD: the values themselves, else NaN.
+template <bool BF16, int D, int R, bool ADD>
+__device__ __forceinline__ void restore(floatx16 (&acc)[D / 32], const char *t, int first, int last, int h) {
   using L = Tile<BF16, D>;
   first = max(first, 0);
   last = min(last, R - 1);
@@ -344,13 +346,15 @@ __device__ __forceinline__ void poison(floatx16 (&acc)[D / 32], const char *t, i
         if constexpr (BF16) {
           const uintx2 w = *reinterpret_cast<const uintx2 *>(t + L::at(r, col >> 3) + 2 * (col & 7));
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (odd(e & 1 ? w[e >> 1] : w[e >> 1] << 16)) acc[b][i + e] = __builtin_nanf("");
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x = e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16;
+            if (odd(x)) acc[b][i + e] = ADD ? acc[b][i + e] + __uint_as_float(x) : __builtin_nanf("");
+          }
         } else {
           const uintx4 w = *reinterpret_cast<const uintx4 *>(t + L::at(r, col >> 2));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (odd(w[e])) acc[b][i + e] = __builtin_nanf("");
+            if (odd(w[e])) acc[b][i + e] = ADD ? acc[b][i + e] + __uint_as_float(w[e]) : __builtin_nanf("");
         }
       }
 }

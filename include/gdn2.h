@@ -701,7 +701,10 @@ gdn2_status gdn2_rotary_backward(const gdn2_rotary_desc *desc, const void *q, co
  * Tensors and strides are 16-byte aligned, lse and offsets 4-byte.
  * Scores, sums and softmax are fp32; with bf16 inputs the probabilities (and
  * their gradients) are rounded to bf16 once as operands of the matrix products,
- * and every output once. NaN and infinities reach exactly the results that see them. */
+ * and every output once. NaN and infinities reach exactly the results that see
+ * them. An infinity in v makes o that infinity, one in dO makes dv that (NaN
+ * where its weight is zero in fp32, or beside the opposite one), and either makes
+ * NaN of the dq and dk that it meets. */
 typedef struct {
   int32_t B, T_q, T_k, H, H_kv, d;
   int32_t causal; /* 0 or 1 */
