@@ -96,6 +96,9 @@ __device__ __forceinline__ int first_key(const DecodeArgs &p, int len) {
   return p.window && len > p.window ? (len - p.window) & ~(kTileKeys - 1) : 0;
 }
 
+// The workspace: maximum and sum of each head's spans, then (from a multiple of 16 bytes on) their outputs.
+__host__ __device__ __forceinline__ int64_t outputs_at(int64_t N, int H, int splits) { return (N * H * splits * 2 + 3) & ~(int64_t)3; }
+
 // ONE: a tile of 32 keys lies in one page.
 template <bool BF16, int D, bool ONE>
 __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_decode_kernel(const DecodeArgs p, const DecodePlan plan, int shift) {
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_decode
       store_f<BF16, 4>(p.o, (size_t)(at * D + d), y);
     } else {
       float *ml = p.workspace + (at * plan.splits + split) * 2;
-      float *to = p.workspace + (int64_t)p.N * p.H * plan.splits * 2 + (at * plan.splits + split) * D + d;
+      float *to = p.workspace + outputs_at(p.N, p.H, plan.splits) + (at * plan.splits + split) * D + d;
       if (d == 0) {
         ml[0] = most;
         ml[1] = l;
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(64 * WAVES) attention_decode_join_kernel(const
   // span 0 is always written
   const int live = max(1, (len - first_key(p, len) + plan.span - 1) / plan.span);
   const float *ml = p.workspace + at * plan.splits * 2;
-  const float *os = p.workspace + (int64_t)p.N * p.H * plan.splits * 2 + at * plan.splits * D + V * lane;
+  const float *os = p.workspace + outputs_at(p.N, p.H, plan.splits) + at * plan.splits * D + V * lane;
   float most = neg_inf();
   for (int s = lane; s < live; s += 64) most = fmaxf(most, ml[2 * s]);
 #pragma unroll
@@ -412,7 +415,7 @@ DecodePlan decode_plan(int N, int H, int Hkv, int M, int page, int window) {
 }
 
 size_t decode_workspace_bytes(const DecodePlan &plan, int N, int H, int d) {
-  return plan.splits == 1 ? 0 : (size_t)N * H * plan.splits * ((size_t)d + 2) * 4;
+  return plan.splits == 1 ? 0 : ((size_t)outputs_at(N, H, plan.splits) + (size_t)N * H * plan.splits * d) * 4;
 }
 
 hipError_t launch_attention_decode(const DecodeArgs &p, hipStream_t stream) {

@@ -211,3 +211,14 @@ def test_store_one_token_each_and_places_that_are_none():
     wk, wv = torch.zeros_like(kc), torch.zeros_like(vc)
     wk[0, :, 15], wk[3, :, 0], wv[0, :, 15], wv[3, :, 0] = k[0, 0], k[1, 0], v[0, 0], v[1, 0]
     assert torch.equal(kc, wk) and torch.equal(vc, wv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,length", [(5, 1, 640), (1, 1, 600), (3, 3, 897)])
+def test_an_odd_number_of_heads_and_spans(H, Hkv, length, d, dtype):
+    """The spans' outputs lie behind an odd number of statistics."""
+    q, kc, vc, pages, ln, toks = problem(H + length, [length], H, Hkv, d, 32, dtype)
+    o = g.attention_decode(q, kc, vc, pages, ln)
+    torch.cuda.synchronize()
+    check(f"decode odd {H} {length}", o, q, toks)
