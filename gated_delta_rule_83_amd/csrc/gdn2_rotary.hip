@@ -7,8 +7,10 @@
 // every row is read once and written once. A lane holds two pieces of 4 values
 // whose pairs it has whole, a row lies on 2 to 32 lanes of a wave, so a wave has
 // several heads of one token at once; its 64 lanes compute the token's sines
-// once for all of its heads. The angle is a product of 55 bits: it is taken in
-// 64 bits and brought within one turn there, then rounded to fp32.
+// once for all of its heads. The angle is a product of 55 bits, times 1 / (2 pi):
+// both products keep what their rounding to 64 bits leaves, so that a turn's
+// fraction is as exact at position 2^31 as at 1 (without, up to 4e-7 of a radian
+// off there); then it is rounded to fp32.
 #include "gdn2_rotary.hpp"
 #include "gdn2_vec.hpp"
 
@@ -18,8 +20,10 @@ namespace {
 constexpr int kWaves = 4;
 
 __device__ __forceinline__ void turn_of(int position, float inv_freq, float *c, float *s) {
-  const double turns = (double)position * (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  const float x = (float)(2.0 * (turns - __builtin_rint(turns)));                     // half turns, -1 .. 1
+  constexpr double kTurn = 0.15915494309189533577, kTurnLow = -9.839338337591243e-18;  // 1 / (2 pi), and the rest of it
+  const double p = position, f = inv_freq, a = p * f, low = __builtin_fma(p, f, -a);  // p f = a + low
+  const double part = __builtin_fma(a, kTurn, -__builtin_rint(a * kTurn));
+  const float x = (float)(2.0 * (part + __builtin_fma(a, kTurnLow, low * kTurn)));  // half turns, -1 .. 1
   sincospif(x, s, c);
 }
 

@@ -642,8 +642,8 @@ typedef enum { GDN2_PAIRS_HALVES = 0, GDN2_PAIRS_NEIGHBOURS = 1 } gdn2_pairs;
  *   (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin)
  *
  * for each pair p, the angle being positions[token] * inv_freq[p], a product
- * that is not rounded before it is brought within one turn: any position is as
- * exact as position 1.
+ * that is brought within one turn before it is rounded: any position is as exact
+ * as position 1.
  *   q, q_out : [tokens, H_q, d]    k, k_out : [tokens, H_k, d]   in dtype
  *   q_weight, k_weight : [d] in wdtype, or NULL (ones)
  *   positions : [tokens] int32     inv_freq : [rot / 2] fp32

@@ -212,3 +212,41 @@ def test_no_epsilon(N, H, Hk, d, dtype):
     torch.cuda.synchronize()
     one("rotary eps 0 q", q, qw, pos, f, 0.0, True, "halves", qo, gq, gr["dq"], gr["dq_weight"])
     one("rotary eps 0 k", k, kw, pos, f, 0.0, True, "halves", ko, gk, gr["dk"], gr["dk_weight"])
+
+
+PI = 31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679821  # times 10^103
+
+
+def turns_of(position, frequency):
+    """The fraction of a turn, -1/2 .. 1/2, of position * frequency, by whole numbers alone."""
+    m = int(float(frequency) * 2 ** 40)  # exact: frequencies of 24 bits from 2^-16 on
+    assert m == float(frequency) * 2 ** 40
+    scaled = position * m * 2 ** 160 * 10 ** 103 // (2 * PI)  # turns * 2^200
+    scaled = (scaled + 2 ** 199) % 2 ** 200 - 2 ** 199
+    return scaled / 2 ** 200
+
+
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+@pytest.mark.parametrize("d", [64, 62])
+def test_far_angles_are_as_exact_as_near_ones(d, pairs):
+    """Sines and cosines themselves (pairs of 1 and 0) at positions near 2^31. The fraction of a turn is rounded once,
+    x half turns by u |x|, and a sine or cosine is off by two units in the last place, 4 u of itself: where the angle is
+    near a whole turn this sees errors far below u."""
+    rng = np.random.default_rng(6)
+    N, half = 96, d // 2
+    pos = np.concatenate((rng.integers(2 ** 31 - 2 ** 20, 2 ** 31, N // 2), rng.integers(-2 ** 31, -2 ** 31 + 2 ** 20, N // 4),
+                          rng.integers(0, 100, N // 4)))
+    f = rng.uniform(0.5, 1, half).astype(np.float32)
+    f[half // 2:] *= np.float32(2.0) ** -rng.integers(0, 15, half - half // 2)
+    q = torch.zeros(N, 1, d, device=DEV)
+    a, b = (slice(0, half), slice(half, d)) if pairs == "halves" else (slice(0, d, 2), slice(1, d, 2))
+    q[..., a] = 1
+    y, _ = g.rotary_forward(q, None, torch.tensor(pos, dtype=torch.int32, device=DEV), torch.tensor(f, device=DEV), norm=False,
+                            pairs=pairs)
+    torch.cuda.synchronize()
+    x = 2 * np.array([[turns_of(int(p), v) for v in f] for p in pos])
+    c, s = np.cos(np.pi * x), np.sin(np.pi * x)
+    assert np.abs(x[:N // 2]).min() < 2.0 ** -8  # some near a whole turn
+    Y = R.f64(y)[:, 0]
+    R.hold("far sines", torch.tensor(Y[:, b]), s, U * (np.pi * np.abs(x) + 4 * np.abs(s)) + 1e-15)
+    R.hold("far cosines", torch.tensor(Y[:, a]), c, U * (np.pi * np.abs(x * s) + 4 * np.abs(c)) + 1e-15)
