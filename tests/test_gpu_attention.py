@@ -404,3 +404,26 @@ def test_offsets_past_32_bits():
     o2, lse2, gr2 = run(q, kv, kv, torch.ones_like(q))
     assert k.stride(1) * T * 2 > 1 << 32
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(gr[n], gr2[n]) for n in gr)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,T,H,Hkv", [(64, 260, 2, 1), (128, 260, 2, 1), (64, 131, 72, 36)])
+def test_gradients_under_large_scores(d, T, H, Hkv, dtype):
+    """Scores of several hundred, so that probabilities come from differences of large numbers: the gradients too are
+    held to their bounds. Sizes for which those hold (a score off by less than 0.02)."""
+    q, k, v, dO = problem(d + T, 1, T, T, H, Hkv, d, dtype)
+    k[0, ::61] *= 30 if d == 64 else 20
+    k[0, :64] *= 4
+    scale = 0.5 if d == 64 else 0.25
+    Q, K = R.f64(q[0]), R.f64(k[0])
+    off = max((np.abs(Q[:, h]) @ np.abs(K[:, h * Hkv // H]).T).max() for h in range(H)) * scale * (d + 8) * R.U
+    assert off < 0.018 and np.abs(scale * Q[:, 0] @ K[:, 0].T).max() > 300
+    o, lse, gr = run(q, k, v, dO, scale=scale)
+    # Probabilities below 2^-126, the smallest normal number of fp32, are zero (they reach e^-1000 here), and so are
+    # products and outputs: an error of 2^-126 in each of the T H probabilities and gradients of scores, times |dp - delta|
+    # of at most twice the largest |dO| |v| sum and the largest factor of the last product, and in each output.
+    size = max(float(x.abs().max()) for x in (q, k, v, dO))
+    under = 2.0 ** -126 * (1 + T * H * 2 * d * size ** 3)
+    ref = R.grouped(q[0], k[0], v[0], dO[0], scale, True, 0, q.dtype)
+    for n, got in (("o", o[0]), ("lse", lse[0]), ("dq", gr["dq"][0]), ("dk", gr["dk"][0]), ("dv", gr["dv"][0])):
+        R.hold(f"large scores d{d} {dtype} {n}", got, ref[n][0], ref[n][1] + under)
