@@ -752,6 +752,7 @@ gdn2_status gdn2_attention_backward_varlen(const gdn2_attention_desc *desc, cons
  * in the cache), sees all of them or (window > 0) the last `window`. Tokens of a
  * page outside [0, P) are not seen; whatever a page holds behind a sequence's last
  * token is not read into any result. A query that sees no token (or scores of -inf alone) gives zeros.
+ * With bf16 inputs a probability keeps 16 bits as an operand of the matrix products; outputs are rounded once.
  *   q, o : [N, H, d]    d 64 or 128; H % H_kv == 0; N * H up to 2^22 - 1, the call's workgroups up to 2^24 - 1
  * The work is split over the longest length that the table has room for; the
  * spans' partial results (fp32) lie in the workspace

@@ -222,3 +222,27 @@ def test_an_odd_number_of_heads_and_spans(H, Hkv, length, d, dtype):
     o = g.attention_decode(q, kc, vc, pages, ln)
     torch.cuda.synchronize()
     check(f"decode odd {H} {length}", o, q, toks)
+
+
+@pytest.mark.parametrize("page", [8, 64])
+@pytest.mark.parametrize("H,Hkv,d,length", [(16, 2, 128, 3000), (4, 4, 64, 400), (8, 1, 64, 70)])
+def test_probabilities_keep_more_than_the_outputs_type(H, Hkv, d, length, page):
+    """bf16: a probability is held as an operand in two parts of 8 bits, off by 2^-15 of itself at most (the second part's
+    rounding, 2^-8 of 2^-7), so a result is off by its own rounding, 2^-8, and next to nothing else."""
+    q, kc, vc, pages, ln, toks = problem(H + length, [length, length // 2], H, Hkv, d, page, "bf16")
+    o = g.attention_decode(q, kc, vc, pages, ln)
+    torch.cuda.synchronize()
+    scale, U, h = float(np.float32(d ** -0.5)), R.U, 2.0 ** -8
+    for n, (k, v) in enumerate(toks):
+        Q, K, V = R.f64(q[n, 0]), R.f64(k), R.f64(v)
+        for head in range(H):
+            a, b = K[:, head * Hkv // H], V[:, head * Hkv // H]
+            s = scale * a @ Q[head]
+            off = scale * (d + 8) * U * (np.abs(a) @ np.abs(Q[head])) + 6 * U * np.abs(s)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            rel = 2.1 * off + 8 * U
+            rel = rel + (p * rel).sum() + (len(s) / 16 + 16) * U + 2.0 ** -15
+            tol = (p * rel) @ np.abs(b) + (len(s) + 16) * U * (p @ np.abs(b))
+            ref = p @ b
+            R.hold(f"decode in two parts {n} {head}", o[n, 0, head], ref, tol + (h + 2 * U) * (np.abs(ref) + tol))
