@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256, BF16 || D == 64 ? 2 : 1) attention_forwar
     if constexpr (BF16) {
 #pragma unroll
       for (int g = 0; g < 2 * SUB; ++g) {
-        // the probabilities' one rounding, 2^-9 of each at most
+        // the probabilities' one rounding, 2^-8 of each at most
         const Frag<BF16> w = operand<BF16>(s[g / 2], g % 2);
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {

@@ -12,7 +12,7 @@
 // at every run. Scores are kept so that the rows of the product to come are the
 // registers: keys for dq, queries for dk and dv.
 //
-// bf16 operands of the last products: p and ds are rounded once, 2^-9 at most,
+// bf16 operands of the last products: p and ds are rounded once, 2^-8 at most,
 // which is the size of the results' own rounding. In tiles of which some places
 // are hidden (the diagonal's: there rows see few keys, and the largest
 // probabilities are) the remainder goes through the product as well: gradients
