@@ -26,6 +26,12 @@ def no_second_order(name):
         raise RuntimeError(f"{name} has no second derivatives (create_graph=True)")
 
 
+def layout_of(*tensors):
+    """Strides of saved tensors: what hooks on them may return otherwise than it
+    was (the same values, sizes and type, laid out as the hook's copy has them)."""
+    return [None if t is None else t.stride() for t in tensors]
+
+
 class launch_on:
     """with launch_on(device, stream) as handle: the tensors' device is current,
     new tensors belong to the launch's stream, and handle is that stream's

@@ -15,7 +15,7 @@ from __future__ import annotations
 import ctypes
 
 from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
-from ._launch import launch_on, no_second_order, want, want_tokens
+from ._launch import launch_on, layout_of, no_second_order, want, want_tokens
 from .linear import _ref, _scratch
 
 
@@ -147,13 +147,13 @@ def _forward(q, k, v, cu_q, cu_k, scale, causal, window, o, lse, stream):
         if lse is None:
             lse = torch.empty(rows, dtype=torch.float32, device=dev)
         _launch_forward(desc, q, k, v, cu_q, cu_k, o, lse, handle)
-    return o, lse
+    return desc, o, lse
 
 
 def attention_forward(q, k, v, scale=None, causal: bool = True, window: int = 0, o=None, lse=None, stream=None):
     """q [B, T_q, H, d], k, v [B, T_k, H_kv, d] (bf16 or fp32, d 64 or 128).
     Returns (o like q, lse [B, H, T_q] fp32)."""
-    return _forward(q, k, v, None, None, scale, causal, window, o, lse, stream)
+    return _forward(q, k, v, None, None, scale, causal, window, o, lse, stream)[1:]
 
 
 def attention_forward_varlen(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, window: int = 0, o=None, lse=None,
@@ -161,7 +161,7 @@ def attention_forward_varlen(q, k, v, cu_q, cu_k=None, scale=None, causal: bool 
     """Packed sequences: q [T_q, H, d], k, v [T_k, H_kv, d], offsets cu_q, cu_k
     (int32, B + 1; cu_k defaults to cu_q). Returns (o, lse [H, T_q]); rows
     outside every sequence are not written."""
-    return _forward(q, k, v, *_offsets(cu_q, cu_k), scale, causal, window, o, lse, stream)
+    return _forward(q, k, v, *_offsets(cu_q, cu_k), scale, causal, window, o, lse, stream)[1:]
 
 
 def _launch_backward(desc, q, k, v, cu_q, cu_k, o, lse, dO, g, workspace, handle):
@@ -286,8 +286,8 @@ def _autograd_function():
 
         @staticmethod
         def forward(ctx, q, k, v, cu_q, cu_k, scale, causal, window):
-            o, lse = _forward(q, k, v, cu_q, cu_k, scale, causal, window, None, None, None)
-            ctx.problem = scale, causal, window
+            ctx.desc, o, lse = _forward(q, k, v, cu_q, cu_k, scale, causal, window, None, None, None)
+            ctx.layout, ctx.problem = layout_of(q, k, v, cu_q, cu_k, o, lse), (scale, causal, window)
             ctx.save_for_backward(q, k, v, cu_q, cu_k, o, lse)
             return o
 
@@ -296,10 +296,11 @@ def _autograd_function():
             # autograd has made the forward's device and stream current
             no_second_order("attention")
             q, k, v, cu_q, cu_k, o, lse = ctx.saved_tensors
-            # hooks on saved tensors may return them laid out otherwise than the forward's
-            desc, dev, rows = _problem(q, k, v, cu_q, cu_k, *ctx.problem)
-            want(o, "o", q.shape, q.dtype, dev)
-            want(lse, "lse", rows, torch.float32, dev)
+            desc = ctx.desc
+            if layout_of(q, k, v, cu_q, cu_k, o, lse) != ctx.layout:  # hooks on saved tensors
+                desc, dev, rows = _problem(q, k, v, cu_q, cu_k, *ctx.problem)
+                want(o, "o", q.shape, q.dtype, dev)
+                want(lse, "lse", rows, torch.float32, dev)
             g = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
             _launch_backward(desc, q, k, v, cu_q, cu_k, o, lse, dO.contiguous(), g, None,
                              torch._C._cuda_getCurrentRawStream(q.device.index))

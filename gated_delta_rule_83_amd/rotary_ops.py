@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 
 from . import GDN2_OK, Gdn2Error, _dtype_code, _ptr, load
-from ._launch import launch_on, no_second_order, want, want_tokens
+from ._launch import launch_on, layout_of, no_second_order, want, want_tokens
 from .linear import _ref, _scratch
 
 PAIRS = {"halves": 0, "neighbours": 1}
@@ -91,7 +91,7 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_
                                  _ptr(q_out), _ptr(k_out) if k is not None else None, handle)
     if st != GDN2_OK:
         raise Gdn2Error(st)
-    return q_out, k_out if k is not None else None
+    return desc, q_out, k_out if k is not None else None
 
 
 def rotary_forward(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
@@ -100,7 +100,7 @@ def rotary_forward(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps:
     tokens lie apart, as of a fused projection, are taken as they are),
     positions [...] int32, inv_freq [rot / 2] fp32, weights [d] of one type or
     None. Returns (q_out, k_out), contiguous."""
-    return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_out, k_out, stream)
+    return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, q_out, k_out, stream)[1:]
 
 
 def rotary_backward(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out, eps: float = 1e-6, norm: bool = True,
@@ -155,8 +155,8 @@ def _autograd_function():
 
         @staticmethod
         def forward(ctx, q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs):
-            qo, ko = _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, None, None, None)
-            ctx.problem = eps, norm, pairs
+            ctx.desc, qo, ko = _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, norm, pairs, None, None, None)
+            ctx.layout, ctx.problem = layout_of(q, k, positions, inv_freq, q_weight, k_weight), (eps, norm, pairs)
             ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
             return qo, ko
 
@@ -165,8 +165,9 @@ def _autograd_function():
             # autograd has made the forward's device and stream current
             no_second_order("rotary")
             q, k, positions, inv_freq, qw, kw = ctx.saved_tensors
-            # hooks on saved tensors may return them laid out otherwise than the forward's
-            desc, _ = _problem(q, k, positions, inv_freq, qw, kw, *ctx.problem)
+            desc = ctx.desc
+            if layout_of(q, k, positions, inv_freq, qw, kw) != ctx.layout:  # hooks on saved tensors
+                desc, _ = _problem(q, k, positions, inv_freq, qw, kw, *ctx.problem)
             new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
             dq, dk = new(q), None if k is None else new(k)
             dqw = new(qw) if ctx.needs_input_grad[4] else None
