@@ -5,7 +5,7 @@
 // of which 16 query heads' products cost the matrix cores little. A workgroup
 // takes a span of one sequence's keys and one key head, a wave every fourth tile
 // of 32 keys, straight from memory to registers, the next tile's loads out before
-// this one's are used (N4 131072 tokens: 111 us without, 88 with, 84 as it stands: 7.1 TB/s and the join):
+// this one's are used (N4 131072 tokens: 111 us without, 88 with, 86 as it stands: 6.9 TB/s and the join):
 //  - scores transposed (keys as rows), 16 x 16: a key's row is an A operand as it
 //    lies, 8 values a lane;
 //  - o transposed, too: row m of block r is channel m D / 16 + r, so a lane's

@@ -412,9 +412,11 @@ __device__ __forceinline__ void find_work(unsigned units, unsigned *unit, unsign
 // first, and a long one near the front is begun when the rest is nearly done. For causal attention of up to 64
 // sequences the blocks are counted by level instead (KEYS: of keys, whose first block is seen by most queries; else of
 // queries, whose last block sees most keys, the prefix included): lane n holds sequence n's blocks nb and its lowest
-// level c, and the level that the rank falls into is found by halves (us, before and so: 8 sequences, the longest 6266 of
-// 32768 tokens, H8/2 d64: forward 247 / 209, backward 827 / 708; 24 of 16384 H16/4 d128: 145 / 143, 542 / 499; 64 of
-// 32768 H16/2: 216 / 220, 806 / 726).
+// level c, and the level that the rank falls into is found by halves. us before / so, forward and backward: 8 sequences of
+// 32768 tokens H8/2 d64, the longest 6266, 250 / 212 and 838 / 723; 24 of 16384 H16/4 d128, the longest 3147, 144 / 143
+// and 556 / 507, the longest 2044, 132 / 121 and 459 / 431, the longest 1469, 119 / 124 and 453 / 428; 64 of 32768 H16/2
+// d128, the longest 1967, 219 / 225 and 820 / 737: where all are short the forward loses 3%, less than the backward
+// of the same sequences gains.
 template <int ROWS, bool KEYS>
 __device__ __forceinline__ bool find_ranked(const AttentionArgs &p, int slots, int rank, int *seq, int *row0) {
   const int32_t *cu = KEYS ? p.cu_k : p.cu_q;
