@@ -643,7 +643,7 @@ typedef enum { GDN2_PAIRS_HALVES = 0, GDN2_PAIRS_NEIGHBOURS = 1 } gdn2_pairs;
  *
  * for each pair p, the angle being positions[token] * inv_freq[p], a product
  * that is brought within one turn before it is rounded: any position is as exact
- * as position 1.
+ * as position 1 (frequencies up to 2^20).
  *   q, q_out : [tokens, H_q, d]    k, k_out : [tokens, H_k, d]   in dtype
  *   q_weight, k_weight : [d] in wdtype, or NULL (ones)
  *   positions : [tokens] int32     inv_freq : [rot / 2] fp32

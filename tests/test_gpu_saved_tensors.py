@@ -65,3 +65,19 @@ def test_rotary(kind, dtype):
     got = finish()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, plain))
+
+
+def test_a_layout_that_no_call_takes_is_refused():
+    """A hook that returns a batch's tokens not one distance apart."""
+    x = torch.randn(2, 30, (H + 2 * HK) * D, device=DEV, requires_grad=True)
+    pos, f = torch.arange(60, dtype=torch.int32, device=DEV).view(2, 30), torch.ones(D // 2, device=DEV)
+
+    def unpack(t):
+        return t.transpose(0, 1).contiguous().transpose(0, 1) if t.dim() == 4 else t
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, unpack):
+        q, k, v = parts(x)
+        outs = g.attention(q, k, v), g.rotary(q, k, pos, f)[0]
+    for y in outs:
+        with pytest.raises(ValueError, match="one distance apart|contiguous"):
+            torch.autograd.grad(y.sum(), x, retain_graph=True)
